@@ -8,12 +8,20 @@ from . import inputs  # noqa: F401
 from .moe355 import (  # noqa: F401
     MoELayer,
     Moe355Error,
+    fp4_dequant_groups,
+    fp4_quant_groups,
     fp8_quant_1x128,
+    gemm_fp4_groupscale,
     gemm_fp8_blockscale,
     gemm_fp8_blockscale_plan,
     gemm_fp8_blockscale_tiled,
     gemm_fp8_blockscale_tiled_workspace,
     gemm_fp8_blockscale_workspace,
+    grouped_gemm,
+    grouped_gemm_dgrad,
+    grouped_gemm_fp4,
+    grouped_gemm_wgrad,
+    grouped_linear,
     grouped_topk,
     lib,
     moe_block_m,

@@ -1,0 +1,58 @@
+// 16-bit MFMA operands and products (gfx950).
+#pragma once
+
+#include "device_common.h"
+
+namespace moe355 {
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+
+// D = A(16x32) * B(32x16) + C, bf16 or fp16 operands, fp32 result.  Lane l holds row/column
+// l % 16 and k slots [8 (l / 16), 8 (l / 16) + 8); output element (4 (l / 16) + i, l % 16) in c[i].
+template <bool F16>
+__device__ __forceinline__ v4f mfma16x16x32(const s16x8& a, const s16x8& b, const v4f& c) {
+  if constexpr (F16) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
+                                                  0);
+  } else {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                   0, 0);
+  }
+}
+
+// Eight e2m1 codes (4 bits each, lowest first) -> eight bf16 or fp16 values times 2^(scale's
+// exponent); every code is exact in both types, and so is the product in bf16.
+template <bool F16>
+__device__ __forceinline__ s16x8 e2m1x8(uint32_t codes, float scale) {
+  u32x4 r;
+  if constexpr (F16) {
+    r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, scale, 0));
+    r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, scale, 1));
+    r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, scale, 2));
+    r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, scale, 3));
+  } else {
+    r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 0));
+    r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 1));
+    r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 2));
+    r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 3));
+  }
+  return __builtin_bit_cast(s16x8, r);
+}
+
+// fp32 value of an E8M0 scale code: 2^(code - 127), NaN for 255
+__device__ __forceinline__ float e8m0_to_f32(uint32_t code) {
+  return __uint_as_float(code == 0 ? 0x00400000u : code == 255u ? 0x7fc00000u : code << 23);
+}
+
+// Segment [lo, hi) of expert e, kept inside [0, R] whatever the offsets hold.
+__device__ __forceinline__ void segment(const int32_t* offsets, int R, int e, int& lo, int& hi) {
+  lo = min(max(offsets[e], 0), R);
+  hi = min(max(offsets[e + 1], lo), R);
+}
+
+}  // namespace moe355

@@ -1,0 +1,382 @@
+// Products grouped by expert over ragged row segments (16-bit operands, fp32 sums)
+// and their two gradients.
+//
+// With C[m, n] = sum_k A(m, k) B(n, k) the three directions are one tiled product:
+//   fwd    m = row of the segment, n = output feature, k = input feature
+//   dgrad  m = row of the segment, n = input feature,  k = output feature
+//   wgrad  m = output feature,     n = input feature,  k = row of the segment
+// An operand whose k runs along its rows in memory is staged as BM (or BN) rows of
+// 64 k and read as 16-byte fragments; one whose m or n runs along memory rows is
+// staged as 64 rows of k and read through the transposing LDS read, so no direction
+// needs a transposed copy of anything.
+//
+// Ragged edges cost no branch in the loop: every LDS-DMA goes through a buffer
+// descriptor that ends with the segment's (or matrix's) last valid byte, so rows past it
+// arrive as zeros, and lanes whose chunk lies past the row's width are sent past the end.
+// Zeros on both operands keep a neighbour expert's infinities and NaN out of the sums.
+#include "ragged_gemm.h"
+
+#include "device_common.h"
+#include "frag16.h"
+#include "gemm_engine.h"
+#include "host_common.h"
+
+namespace moe355 {
+namespace {
+
+constexpr int kBK = 64;                      // k per step
+constexpr uint32_t kPastEnd = 0x80000000u;   // a lane offset beyond every descriptor's length
+
+// LDS-DMA through a buffer descriptor: lane l moves 16 bytes from base + off to
+// LDS[m0 + 16 l]; off at or past the descriptor's length writes zeros.
+__device__ __forceinline__ void dma16_buf(u32x4 rsrc, uint32_t off, uint32_t m0) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(off), "s"(rsrc), "s"(m0)
+               : "memory");
+}
+
+__device__ __forceinline__ u32x4 buffer_of(const void* base, uint32_t bytes) {
+  const uint64_t v = reinterpret_cast<uint64_t>(base);
+  return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)v),
+               (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(v >> 32)) & 0xffffu,
+               (uint32_t)__builtin_amdgcn_readfirstlane(bytes), 0x00020000u};
+}
+
+// Rotation of the 32-byte column pairs of k-row r in a tile read transposed: the 8 k-rows
+// that half a wave touches in one read land in different banks.
+__device__ __forceinline__ int tr_swz(int r) { return (r & 3) | ((r >> 1) & 4); }
+
+// One operand of the tile: ROWS rows of m (or n); KMAJOR: k runs along memory rows.
+// NW waves fill it with NI DMA instructions each.
+template <int ROWS, int NW, bool KMAJOR>
+struct Operand {
+  static constexpr int kBytes = ROWS * kBK * 2;
+  static constexpr int NI = kBytes / 1024 / NW;
+  uint32_t off[NI];  // byte offsets of this lane's chunks in a step
+  int kc;            // KMAJOR: this lane's k within the step
+
+  __device__ __forceinline__ void init(int w, int lane, int64_t ld, int cols) {
+    if constexpr (KMAJOR) {
+      const int c = (lane & 7) ^ (lane >> 3);
+      kc = 8 * c;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) off[i] = (uint32_t)((8 * (w * NI + i) + (lane >> 3)) * (ld * 2) + c * 16);
+    } else {
+      constexpr int CPR = ROWS / 8;  // 16-byte chunks per k-row
+      kc = 0;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int r = (w * NI + i) * (64 / CPR) + lane / CPR;
+        const int c = (lane % CPR) ^ (tr_swz(r) << 1);
+        off[i] = 8 * c < cols ? (uint32_t)(r * (ld * 2) + c * 16) : kPastEnd;
+      }
+    }
+  }
+  // krem: k left from this step's first on
+  __device__ __forceinline__ void fetch(u32x4 rsrc, uint32_t lds, int w, int krem) const {
+    const uint32_t past = KMAJOR && kc >= krem ? kPastEnd : 0u;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) dma16_buf(rsrc, off[i] | past, lds + (w * NI + i) * 1024);
+  }
+};
+
+// Fragments of 16 rows x 32 k (lane l: row l % 16, k 8 (l / 16) .. + 7) of a staged operand.
+template <int ROWS, bool KMAJOR, int T>
+struct Fragments {
+  uint32_t at[KMAJOR ? 2 : T];  // KMAJOR: per half step; else per fragment
+
+  __device__ __forceinline__ void init(int row0, int lane) {
+    const int i = lane & 15, g = lane >> 4;
+    if constexpr (KMAJOR) {
+      at[0] = (row0 + i) * 128 + ((g ^ (i & 7)) << 4);
+      at[1] = at[0] ^ 64;
+    } else {
+      const int r = 8 * g + (i >> 2);
+#pragma unroll
+      for (int f = 0; f < T; ++f) at[f] = r * (2 * ROWS) + ((((row0 >> 4) + f) ^ tr_swz(r)) << 5) + (i & 3) * 8;
+    }
+  }
+  __device__ __forceinline__ s16x8 read(uint32_t lds, int f, int half) const {
+    typedef __attribute__((address_space(3))) s16x8* p8;
+    typedef __attribute__((address_space(3))) s16x4* p4;
+    if constexpr (KMAJOR) {
+      return *reinterpret_cast<p8>(lds + at[half] + f * 2048);
+    } else {
+      const uint32_t a = lds + at[f] + half * (32 * 2 * ROWS);
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<p4>(a));
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<p4>(a + 4 * 2 * ROWS));
+      return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+  }
+};
+
+// Row tiles of expert e.
+__device__ __forceinline__ int row_tiles(const int32_t* offsets, int R, int e, int BM) {
+  int lo, hi;
+  segment(offsets, R, e, lo, hi);
+  return (hi - lo + BM - 1) / BM;
+}
+
+// A workgroup's place: expert, row tile and column tile.  Workgroups go to the 8 XCDs in turn, so
+// each XCD takes a contiguous run of the tiles, and inside an expert the tiles advance in
+// bands of 8 row tiles: the tiles that an XCD works on at a time share few panels.
+template <int BM>
+__device__ __forceinline__ bool place(const RaggedArgs& g, int ntiles, int* sh, int& e, int& mt, int& nt) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  if (tid < 64) {
+    const int per = (g.E + 63) / 64;
+    const int e0 = min(g.E, lane * per), e1 = min(g.E, e0 + per);
+    int mine = 0;
+    for (int i = e0; i < e1; ++i) mine += row_tiles(g.offsets, g.R, i, BM);
+    int upto = mine;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int v = __shfl_up(upto, o, 64);
+      if (lane >= o) upto += v;
+    }
+    const int rows = __shfl(upto, 63, 64);
+    const int64_t total = (int64_t)rows * ntiles, chunk = (total + 7) / 8;
+    const int64_t t = (int64_t)(blockIdx.x & 7) * chunk + (blockIdx.x >> 3);
+    if (lane == 0) sh[0] = -1;
+    if ((blockIdx.x >> 3) < chunk && t < total) {
+      // the lane whose experts hold tile t: tiles before this lane's experts are (upto - mine) * ntiles
+      const int64_t first = (int64_t)(upto - mine) * ntiles;
+      if (t >= first && t < (int64_t)upto * ntiles) {
+        int64_t rest = t - first;
+        for (int i = e0; i < e1; ++i) {
+          const int m = row_tiles(g.offsets, g.R, i, BM);
+          if (rest < (int64_t)m * ntiles) {
+            const int band = 8 * ntiles, b0 = (int)(rest / band) * 8, in = (int)(rest % band);
+            const int height = min(8, m - b0);
+            sh[0] = i;
+            sh[1] = b0 + in % height;
+            sh[2] = in / height;
+            break;
+          }
+          rest -= (int64_t)m * ntiles;
+        }
+      }
+    }
+  }
+  __syncthreads();
+  e = sh[0];
+  mt = sh[1];
+  nt = sh[2];
+  return e >= 0;
+}
+
+template <int OP, bool F16, bool OUT32, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN, 2) void ragged_gemm_kernel(RaggedArgs g) {
+  constexpr bool AK = OP != kRaggedWgrad, BK = OP == kRaggedFwd;  // k along memory rows
+  constexpr int NW = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
+  using OA = Operand<BM, NW, AK>;
+  using OB = Operand<BN, NW, BK>;
+  constexpr int kStage = OA::kBytes + OB::kBytes;
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+
+  const int mdim = OP == kRaggedWgrad ? g.N : 0, ndim = OP == kRaggedFwd ? g.N : g.K;
+  const int ntiles = (ndim + BN - 1) / BN;
+  int e, mt, nt, lo, hi;
+  if constexpr (OP == kRaggedWgrad) {
+    const int mtiles = (mdim + BM - 1) / BM;
+    const int64_t total = (int64_t)g.E * mtiles * ntiles, chunk = (total + 7) / 8;
+    const int64_t t = (int64_t)(blockIdx.x & 7) * chunk + (blockIdx.x >> 3);
+    if ((blockIdx.x >> 3) >= chunk || t >= total) return;
+    e = (int)(t / ((int64_t)mtiles * ntiles));
+    const int in = (int)(t - (int64_t)e * mtiles * ntiles), band = 8 * ntiles, b0 = in / band * 8;
+    const int height = min(8, mtiles - b0);
+    mt = b0 + in % band % height;
+    nt = in % band / height;
+  } else {
+    if (!place<BM>(g, ntiles, reinterpret_cast<int*>(smem), e, mt, nt)) return;
+    __syncthreads();  // the place has been read: the DMAs may overwrite it
+  }
+  e = __builtin_amdgcn_readfirstlane(e);
+  mt = __builtin_amdgcn_readfirstlane(mt);
+  nt = __builtin_amdgcn_readfirstlane(nt);
+  segment(g.offsets, g.R, e, lo, hi);
+  lo = __builtin_amdgcn_readfirstlane(lo);
+  hi = __builtin_amdgcn_readfirstlane(hi);
+
+  const int m0 = mt * BM, n0 = nt * BN;
+  const int kdim = OP == kRaggedFwd ? g.K : OP == kRaggedDgrad ? g.N : hi - lo;
+  const int mrows = OP == kRaggedWgrad ? mdim - m0 : hi - lo - m0;  // m left from the tile's first on
+  const int nrows = ndim - n0;
+
+  // first byte of the tile's operands, what a step of 64 k adds, and bytes from there to the end
+  const uint16_t* pa = AK ? g.a + (int64_t)(lo + m0) * g.lda : g.a + (int64_t)lo * g.lda + m0;
+  const uint16_t* pb = OP == kRaggedFwd     ? g.b + ((int64_t)e * g.N + n0) * g.ldb
+                       : OP == kRaggedDgrad ? g.b + (int64_t)e * g.N * g.ldb + n0
+                                            : g.b + (int64_t)lo * g.ldb + n0;
+  const int64_t stepa = AK ? kBK : kBK * g.lda, stepb = BK ? kBK : kBK * g.ldb;
+  int64_t lena = AK ? (min(mrows, BM) - 1) * g.lda + kdim : (kdim - 1) * g.lda + mrows;
+  int64_t lenb = BK ? (min(nrows, BN) - 1) * g.ldb + kdim : (kdim - 1) * g.ldb + nrows;
+
+  OA oa;
+  OB ob;
+  oa.init(w, lane, g.lda, mrows);
+  ob.init(w, lane, g.ldb, nrows);
+  Fragments<BM, AK, TM> fa;
+  Fragments<BN, BK, TN> fb;
+  fa.init((w / WN) * (BM / WM), lane);
+  fb.init((w % WN) * (BN / WN), lane);
+  const uint32_t lds0 = lds_addr(smem);
+
+  v4f acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+
+  const int steps = (kdim + kBK - 1) / kBK;
+  int fetched = 0;
+  auto fetch = [&](uint32_t stage) {  // DMAs of the next step into a stage; past the last step none
+    if (fetched < steps) {
+      const int krem = kdim - fetched * kBK;
+      oa.fetch(buffer_of(pa, (uint32_t)min(lena * 2, (int64_t)0x7ffffff0)), stage, w, krem);
+      ob.fetch(buffer_of(pb, (uint32_t)min(lenb * 2, (int64_t)0x7ffffff0)), stage + OA::kBytes, w, krem);
+      pa += stepa;
+      pb += stepb;
+      lena -= stepa;
+      lenb -= stepb;
+    }
+    ++fetched;
+  };
+  s16x8 ra[2][TM], rb[2][TN];
+  auto load = [&](uint32_t stage, int half) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i) ra[half][i] = fa.read(stage, i, half);
+#pragma unroll
+    for (int j = 0; j < TN; ++j) rb[half][j] = fb.read(stage + OA::kBytes, j, half);
+  };
+  auto multiply = [&](int half) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) acc[i][j] = mfma16x16x32<F16>(rb[half][j], ra[half][i], acc[i][j]);
+  };
+
+  if (steps > 0) {
+    fetch(lds0);
+    vm_wait<0>();
+    barrier_only();
+    fetch(lds0 + kStage);
+    load(lds0, 0);
+    lgkm_wait0();
+    uint32_t cur = lds0, other = lds0 + kStage;
+    for (int s = 0; s < steps; ++s) {
+      // first half: its fragments are in registers; read the second half's meanwhile
+      load(cur, 1);
+      multiply(0);
+      lgkm_wait0();
+      vm_wait<0>();    // this wave's share of the next step has landed
+      barrier_only();  // everyone's has, and nobody reads `cur` any more
+      fetch(cur);
+      load(other, 0);  // of the step after the last: stale values, not used
+      multiply(1);
+      lgkm_wait0();
+      const uint32_t t = cur;
+      cur = other;
+      other = t;
+    }
+    vm_wait<0>();
+  }
+
+  // lane: row m of the tile, four adjacent n
+  const int mw = (w / WN) * (BM / WM) + (lane & 15), nw = (w % WN) * (BN / WN) + 4 * (lane >> 4);
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    const int m = mw + 16 * i;
+    if (m >= mrows) continue;
+    const int64_t row = (OP == kRaggedWgrad ? (int64_t)e * g.N : (int64_t)lo) + m0 + m;
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      const int n = nw + 16 * j;
+      if (n >= nrows) continue;  // nrows % 8 == 0: the four are all in or all out
+      const int64_t at = row * g.ldc + n0 + n;
+      if constexpr (OUT32) {
+        *reinterpret_cast<v4f*>(reinterpret_cast<float*>(g.c) + at) = acc[i][j];
+      } else {
+        const uint2 r{f32_to_out16(acc[i][j][0], F16) | (f32_to_out16(acc[i][j][1], F16) << 16),
+                      f32_to_out16(acc[i][j][2], F16) | (f32_to_out16(acc[i][j][3], F16) << 16)};
+        *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(g.c) + at) = r;
+      }
+    }
+  }
+}
+
+template <int OP, bool F16, bool OUT32, int BM, int BN, int WM, int WN>
+int launch(const RaggedArgs& g, hipStream_t stream) {
+  auto* fn = &ragged_gemm_kernel<OP, F16, OUT32, BM, BN, WM, WN>;
+  constexpr int kLds = 2 * (BM + BN) * kBK * 2;
+  const int64_t nt = ceil_div64(OP == kRaggedFwd ? g.N : g.K, BN);
+  // an upper bound of the row tiles: the offsets are on the device
+  const int64_t mt = OP == kRaggedWgrad ? (int64_t)g.E * ceil_div64(g.N, BM)
+                                        : g.R / BM + (g.E < g.R ? g.E : g.R);
+  const int64_t grid = ceil_div64(mt * nt, 8) * 8;
+  MOE355_CHECK(grid < (1ll << 31), MOE355_EUNSUPPORTED);
+  if (hipFuncSetAttribute(reinterpret_cast<const void*>(fn), hipFuncAttributeMaxDynamicSharedMemorySize, kLds) !=
+      hipSuccess)
+    return MOE355_ELAUNCH;
+  hipLaunchKernelGGL(fn, dim3((unsigned)grid), dim3(64 * WM * WN), kLds, stream, g);
+  return launch_status();
+}
+
+template <int OP, bool OUT32 = false>
+int run(const RaggedArgs& g, int f16, hipStream_t stream) {
+  return f16 ? launch<OP, true, OUT32, 256, 256, 2, 4>(g, stream) : launch<OP, false, OUT32, 256, 256, 2, 4>(g, stream);
+}
+
+bool aligned_rows(const void* p, int64_t ld) { return aligned16(p) && ld % 8 == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Checks the arguments that the three calls share.
+int check(int fp16, int R, int E, int N, int K) {
+  MOE355_CHECK((fp16 == 0 || fp16 == 1) && R >= 0 && E >= 0 && N >= 0 && K >= 0, MOE355_EINVAL);
+  MOE355_CHECK(N % 8 == 0 && K % 8 == 0 && E < 65536, MOE355_EUNSUPPORTED);
+  return MOE355_OK;
+}
+
+constexpr int64_t kMaxLd = 1 << 21;  // 256 rows' byte offsets stay below 2^31
+
+}  // namespace
+}  // namespace moe355
+
+using namespace moe355;
+
+extern "C" int grouped_gemm(const uint16_t* x, int fp16, int64_t ld_x, const uint16_t* w, const int32_t* offsets, int R,
+                            int E, int N, int K, uint16_t* y, int64_t ld_y, hipStream_t stream) {
+  if (int st = check(fp16, R, E, N, K)) return st;
+  MOE355_CHECK(ld_x >= K && ld_y >= N, MOE355_EINVAL);
+  MOE355_CHECK(ld_x <= kMaxLd && ld_y <= kMaxLd, MOE355_EUNSUPPORTED);
+  if (R == 0 || E == 0 || N == 0) return MOE355_OK;
+  MOE355_CHECK(offsets && y && (K == 0 || (x && w)), MOE355_EINVAL);
+  MOE355_CHECK((K == 0 || (aligned_rows(x, ld_x) && aligned16(w))) && aligned_rows(y, ld_y) && aligned4(offsets), MOE355_EMISALIGNED);
+  return run<kRaggedFwd>(RaggedArgs{x, w, y, offsets, ld_x, K, ld_y, R, E, N, K}, fp16, stream);
+}
+
+extern "C" int grouped_gemm_dgrad(const uint16_t* dy, int fp16, int64_t ld_dy, const uint16_t* w,
+                                  const int32_t* offsets, int R, int E, int N, int K, uint16_t* dx, int64_t ld_dx,
+                                  hipStream_t stream) {
+  if (int st = check(fp16, R, E, N, K)) return st;
+  MOE355_CHECK(ld_dy >= N && ld_dx >= K, MOE355_EINVAL);
+  MOE355_CHECK(ld_dy <= kMaxLd && ld_dx <= kMaxLd, MOE355_EUNSUPPORTED);
+  if (R == 0 || E == 0 || K == 0) return MOE355_OK;
+  MOE355_CHECK(offsets && dx && (N == 0 || (dy && w)), MOE355_EINVAL);
+  MOE355_CHECK((N == 0 || (aligned_rows(dy, ld_dy) && aligned16(w))) && aligned_rows(dx, ld_dx) && aligned4(offsets), MOE355_EMISALIGNED);
+  return run<kRaggedDgrad>(RaggedArgs{dy, w, dx, offsets, ld_dy, K, ld_dx, R, E, N, K}, fp16, stream);
+}
+
+extern "C" int grouped_gemm_wgrad(const uint16_t* dy, int fp16, int64_t ld_dy, const uint16_t* x, int64_t ld_x,
+                                  const int32_t* offsets, int R, int E, int N, int K, void* dw, int out_fp32,
+                                  hipStream_t stream) {
+  if (int st = check(fp16, R, E, N, K)) return st;
+  MOE355_CHECK((out_fp32 == 0 || out_fp32 == 1) && ld_dy >= N && ld_x >= K, MOE355_EINVAL);
+  MOE355_CHECK(ld_dy <= kMaxLd && ld_x <= kMaxLd, MOE355_EUNSUPPORTED);
+  if (E == 0 || N == 0 || K == 0) return MOE355_OK;  // without rows every gradient is zero: still written
+  MOE355_CHECK(offsets && dw && (R == 0 || (dy && x)), MOE355_EINVAL);
+  MOE355_CHECK((R == 0 || (aligned_rows(dy, ld_dy) && aligned_rows(x, ld_x))) && aligned16(dw) && aligned4(offsets), MOE355_EMISALIGNED);
+  const RaggedArgs g{dy, x, dw, offsets, ld_dy, ld_x, K, R, E, N, K};
+  return out_fp32 ? run<kRaggedWgrad, true>(g, fp16, stream) : run<kRaggedWgrad>(g, fp16, stream);
+}

@@ -44,6 +44,13 @@ _SIGNATURES = {
                                   ctypes.POINTER(ctypes.c_int)], _i32),
     "moe_fp8_blockscale_fused": ([_vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32,
                                   _i32, _i32, _i64, _vp, _vp, _i64, _vp, _sz, _vp], _i32),
+    "fp4_quant_groups": ([_vp, _i32, _i64, _i64, _i32, _i32, _vp, _vp, _i32, _vp], _i32),
+    "fp4_dequant_groups": ([_vp, _vp, _i32, _i64, _i32, _i32, _vp, _i32, _i64, _vp], _i32),
+    "gemm_fp4_groupscale": ([_vp, _i32, _i64, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _i64, _vp], _i32),
+    "grouped_gemm_fp4": ([_vp, _i32, _i64, _vp, _vp, _i32, _i32, _vp, _i32, _i32, _i32, _i32, _vp, _i64, _vp], _i32),
+    "grouped_gemm": ([_vp, _i32, _i64, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _i64, _vp], _i32),
+    "grouped_gemm_dgrad": ([_vp, _i32, _i64, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _i64, _vp], _i32),
+    "grouped_gemm_wgrad": ([_vp, _i32, _i64, _vp, _i64, _vp, _i32, _i32, _i32, _i32, _vp, _i32, _vp], _i32),
 }
 # the pre-shuffled-weight variants take the same arguments as their plain calls
 for _name in ("gemm_fp8_blockscale", "moe_fp8_blockscale_g1u1", "moe_down_combine"):
@@ -438,6 +445,183 @@ def gemm_fp8_blockscale(a8, a_scale, b8, b_scale, c=None, scale_layout="row", wo
     _check(fn(_ptr(a8), _ptr(a_scale), ssm, sskb, _ptr(b8), _ptr(b_scale), M, N, K, _ptr(c), _rows(c, "c"),
               int(c.dtype == torch.float16), ws_ptr, ws_n, _stream()))
     return c
+
+
+# ----------------------------------------------------------------- 4-bit weights, ragged groups
+_F16 = {torch.bfloat16: 0, torch.float16: 1}
+
+
+def _half(t, name):
+    """0 for a bf16 device tensor, 1 for an fp16 one."""
+    if not t.is_cuda:
+        raise ValueError("%s must be a GPU tensor" % name)
+    if t.dtype not in _F16:
+        raise ValueError("%s must be bf16 or fp16, got %s" % (name, t.dtype))
+    return _F16[t.dtype]
+
+
+def _out(t, shape, dtype, like, name):
+    """The output tensor: allocated when None, else checked (2-D outputs may have strided rows)."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    _dev(t, dtype, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    return t
+
+
+def _fp4_scale(scale, shape, name="scale"):
+    """0 for fp32 scales, 1 for E8M0 bytes, of this shape."""
+    e8m0 = int(scale.dtype == torch.uint8)
+    _need(scale, shape, torch.uint8 if e8m0 else torch.float32, name)
+    return e8m0
+
+
+def _groups(K, group):
+    if group not in (32, 64, 128):
+        raise ValueError("group must be 32, 64 or 128, got %s" % (group,))
+    return -(-K // group)
+
+
+def fp4_quant_groups(w, group=128, scale_format="fp32", q=None, scale=None):
+    """Pack bf16 or fp16 weights [..., K] to 4 bits: (codes uint8 [..., K/2], scales [..., ceil(K/group)]).
+
+    scale_format "fp32": fp32 scales amax/6; "e8m0": uint8 power-of-two scales (OCP MX with group 32).
+    K % 32 == 0; w contiguous, or 2-D with strided rows.
+    """
+    f16 = _half(w, "w")
+    if scale_format not in ("fp32", "e8m0"):
+        raise ValueError("scale_format must be 'fp32' or 'e8m0'")
+    lead, K = w.shape[:-1], w.shape[-1]
+    if w.dim() != 2 and not w.is_contiguous():
+        raise ValueError("w must be contiguous, or 2-D with contiguous rows")
+    ld = _rows(w, "w") if w.dim() == 2 else K
+    rows = lead.numel()
+    G, e8m0 = _groups(K, group), scale_format == "e8m0"
+    q = _need(_out(q, (*lead, K // 2), torch.uint8, w, "q"), (*lead, K // 2), torch.uint8, "q")
+    sdt = torch.uint8 if e8m0 else torch.float32
+    scale = _need(_out(scale, (*lead, G), sdt, w, "scale"), (*lead, G), sdt, "scale")
+    _check(lib().fp4_quant_groups(_ptr(w), f16, ld if rows > 1 else K, rows, K, group, _ptr(q), _ptr(scale), int(e8m0),
+                                  _stream()))
+    return q, scale
+
+
+def fp4_dequant_groups(q, scale, group=128, dtype=torch.bfloat16, out=None):
+    """Unpack fp4_quant_groups' output to bf16 or fp16 weights [..., K]."""
+    _dev(q, torch.uint8, "q")
+    lead, K = q.shape[:-1], 2 * q.shape[-1]
+    _need(q, q.shape, torch.uint8, "q")
+    e8m0 = _fp4_scale(scale, (*lead, _groups(K, group)))
+    out = _out(out, (*lead, K), dtype, q, "out")
+    f16 = _half(out, "out")
+    if out.dim() != 2 and not out.is_contiguous():
+        raise ValueError("out must be contiguous, or 2-D with contiguous rows")
+    rows = lead.numel()
+    ld = _rows(out, "out") if out.dim() == 2 and rows > 1 else K
+    _check(lib().fp4_dequant_groups(_ptr(q), _ptr(scale), e8m0, rows, K, group, _ptr(out), f16, ld, _stream()))
+    return out
+
+
+def _ld(t, name):
+    """Row stride of a 2-D tensor; of a single row (whose stride means nothing) its width."""
+    ld = _rows(t, name)
+    return ld if t.shape[0] > 1 else t.shape[1]
+
+
+def gemm_fp4_groupscale(x, q, scale, group=128, c=None):
+    """x bf16 or fp16 [M, K] times 4-bit weights q [N, K/2] with scales [N, ceil(K/group)] (fp32, or
+    uint8 for E8M0), transposed: [M, N] in the type of x."""
+    f16 = _half(x, "x")
+    M, K = x.shape
+    N = q.shape[0]
+    _need(q, (N, K // 2), torch.uint8, "q")
+    e8m0 = _fp4_scale(scale, (N, _groups(K, group)))
+    c = _out(c, (M, N), x.dtype, x, "c")
+    _check(lib().gemm_fp4_groupscale(_ptr(x), f16, _ld(x, "x"), _ptr(q), _ptr(scale), e8m0, group, M, N, K, _ptr(c),
+                                     _ld(c, "c"), _stream()))
+    return c
+
+
+def grouped_gemm_fp4(x, q, scale, offsets, group=128, c=None):
+    """Rows of x [R, K] ordered by expert, expert e owning rows [offsets[e], offsets[e+1]) (int32 device
+    tensor [E+1]), times its 4-bit weights q [E, N, K/2] with scales [E, N, ceil(K/group)]: [R, N]."""
+    f16 = _half(x, "x")
+    R, K = x.shape
+    E, N, _ = q.shape
+    _need(q, (E, N, K // 2), torch.uint8, "q")
+    e8m0 = _fp4_scale(scale, (E, N, _groups(K, group)))
+    _need(offsets, (E + 1,), torch.int32, "offsets")
+    c = _out(c, (R, N), x.dtype, x, "c")
+    _check(lib().grouped_gemm_fp4(_ptr(x), f16, _ld(x, "x"), _ptr(q), _ptr(scale), e8m0, group, _ptr(offsets), R, E, N,
+                                  K, _ptr(c), _ld(c, "c"), _stream()))
+    return c
+
+
+def grouped_gemm(x, w, offsets, y=None):
+    """Rows of x [R, K] ordered by expert (offsets int32 [E+1] on the device) times the experts'
+    weights w [E, N, K], transposed: [R, N].  bf16 or fp16; not differentiable (grouped_linear is)."""
+    f16 = _half(x, "x")
+    R, K = x.shape
+    E, N, _ = w.shape
+    _need(w, (E, N, K), x.dtype, "w")
+    _need(offsets, (E + 1,), torch.int32, "offsets")
+    y = _out(y, (R, N), x.dtype, x, "y")
+    _check(lib().grouped_gemm(_ptr(x), f16, _ld(x, "x"), _ptr(w), _ptr(offsets), R, E, N, K, _ptr(y), _ld(y, "y"),
+                              _stream()))
+    return y
+
+
+def grouped_gemm_dgrad(dy, w, offsets, dx=None):
+    """Gradient of grouped_gemm for x: dy [R, N], w [E, N, K] -> [R, K]."""
+    f16 = _half(dy, "dy")
+    R, N = dy.shape
+    E, _, K = w.shape
+    _need(w, (E, N, K), dy.dtype, "w")
+    _need(offsets, (E + 1,), torch.int32, "offsets")
+    dx = _out(dx, (R, K), dy.dtype, dy, "dx")
+    _check(lib().grouped_gemm_dgrad(_ptr(dy), f16, _ld(dy, "dy"), _ptr(w), _ptr(offsets), R, E, N, K, _ptr(dx),
+                                    _ld(dx, "dx"), _stream()))
+    return dx
+
+
+def grouped_gemm_wgrad(dy, x, offsets, dw=None, out_dtype=None):
+    """Gradient of grouped_gemm for w: dy [R, N], x [R, K] -> [E, N, K] in the type of x, or fp32
+    (out_dtype, or the type of dw when given).  Experts without rows get zeros."""
+    f16 = _half(dy, "dy")
+    R, N = dy.shape
+    _dev(x, dy.dtype, "x")
+    if x.dim() != 2 or x.shape[0] != R:
+        raise ValueError("x must be [R, K] with the rows of dy")
+    K, E = x.shape[1], offsets.shape[0] - 1
+    _need(offsets, (E + 1,), torch.int32, "offsets")
+    dt = dw.dtype if dw is not None else out_dtype if out_dtype is not None else x.dtype
+    if dt not in (x.dtype, torch.float32):
+        raise ValueError("dw must be %s or fp32, got %s" % (x.dtype, dt))
+    dw = _need(_out(dw, (E, N, K), dt, x, "dw"), (E, N, K), dt, "dw")
+    _check(lib().grouped_gemm_wgrad(_ptr(dy), f16, _ld(dy, "dy"), _ptr(x), _ld(x, "x"), _ptr(offsets), R, E, N, K,
+                                    _ptr(dw), int(dt == torch.float32), _stream()))
+    return dw
+
+
+class _GroupedLinear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, offsets):
+        ctx.save_for_backward(x, w, offsets)
+        return grouped_gemm(x, w, offsets)
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, w, offsets = ctx.saved_tensors
+        dy = dy.contiguous()
+        dx = grouped_gemm_dgrad(dy, w, offsets) if ctx.needs_input_grad[0] else None
+        dw = grouped_gemm_wgrad(dy, x, offsets) if ctx.needs_input_grad[1] else None
+        return dx, dw, None
+
+
+def grouped_linear(x, w, offsets):
+    """grouped_gemm with gradients for x and w.  Every row of x must lie in a segment
+    (offsets[0] == 0 and offsets[E] == R): rows in none have no defined output or gradient."""
+    return _GroupedLinear.apply(x, w, offsets)
 
 
 # ----------------------------------------------------------------- the layer

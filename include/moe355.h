@@ -350,6 +350,78 @@ int moe_down_combine_wpreshuffle(const uint8_t* h8, const float* h_scale,
                                  uint16_t* out, int64_t ld_out, void* workspace, size_t workspace_bytes,
                                  hipStream_t stream);
 
+/*
+ * 4-bit weights with group scales (OCP e2m1: sign, values 0 .5 1 1.5 2 3 4 6).  A weight row
+ * of K values is K/2 bytes, value k in the low (k even) or high (k odd) half of byte k/2,
+ * and one scale per group of 32, 64 or 128 along K (the last group of a row may be
+ * shorter): value = e2m1(code) * scale.  Scales are fp32, or (e8m0 = 1) one byte c that
+ * stands for 2^(c - 127), 255 for NaN.  G = ceil(K / group); scales are [rows, G].
+ *
+ * fp4_quant_groups packs w [rows, K] (bf16 bits, fp16 bits when fp16 is 1; row stride ld_w):
+ *   fp32 scale = fl32(amax / 6), 1 for an all-zero group;
+ *   e8m0 scale = 2^(floor(log2 amax) - 2), exponent kept in [-127, 127], 1 for an all-zero group;
+ *   code = nearest e2m1 of fl32(w / scale): ties to the even code, saturating at +-6, sign
+ *   kept.  A group that holds a NaN or an infinity gets a NaN scale.
+ * fp4_dequant_groups unpacks: w = bf16 or fp16 nearest of fl32(e2m1(code) * scale).
+ * An expert tensor [E, N, K] is passed as rows = E*N.
+ * K % 32 == 0 and group in {32, 64, 128}, else MOE355_EUNSUPPORTED; w (rows too) and q
+ * 16-byte aligned, else MOE355_EMISALIGNED.
+ */
+int fp4_quant_groups(const uint16_t* w, int fp16, int64_t ld_w, int64_t rows, int K, int group,
+                     uint8_t* q, void* scale, int e8m0, hipStream_t stream);
+int fp4_dequant_groups(const uint8_t* q, const void* scale, int e8m0, int64_t rows, int K, int group,
+                       uint16_t* w, int fp16, int64_t ld_w, hipStream_t stream);
+
+/*
+ * Linear layer on 4-bit weights, for few rows (decode):
+ *   c[m, n] = round(sum_g scale[n, g] * sum_{k in group g} x[m, k] * e2m1(q[n, k]))
+ * x      [M, K] bf16 bits, or fp16 bits when fp16 is 1; row stride ld_x, rows 16-byte aligned.
+ * q      [N, K/2] and scale [N, G] as fp4_quant_groups writes them.
+ * c      [M, N] out, the type of x, row stride ldc >= N; fp32 sums, nearest even.
+ * Any M and N; the time is the weights' bytes up to about 64 rows, beyond that the weights are
+ * read again for every 64 rows.  K % 32 == 0, else MOE355_EUNSUPPORTED.
+ * The result does not depend on timing: every sum has a fixed order.
+ */
+int gemm_fp4_groupscale(const uint16_t* x, int fp16, int64_t ld_x, const uint8_t* q, const void* scale,
+                        int e8m0, int group, int M, int N, int K, uint16_t* c, int64_t ldc,
+                        hipStream_t stream);
+
+/*
+ * Ragged groups: the R rows of x are ordered by expert and expert e owns rows
+ * [offsets[e], offsets[e+1]) of them.  offsets is int32 [E+1] on the DEVICE, does not decrease
+ * and stays in [0, R]; rows in no segment are neither read nor written.  (Offsets outside
+ * [0, R] or decreasing ones are cut to it: nothing outside the buffers is touched, but the rows
+ * concerned are unspecified.)  Experts without rows cost nothing.
+ *
+ * grouped_gemm_fp4: c[r, n] = the 4-bit linear layer above with expert e's q [E, N, K/2] and
+ * scale [E, N, G].  Same types, rules and errors.  E < 65536.
+ */
+int grouped_gemm_fp4(const uint16_t* x, int fp16, int64_t ld_x, const uint8_t* q, const void* scale,
+                     int e8m0, int group, const int32_t* offsets, int R, int E, int N, int K,
+                     uint16_t* c, int64_t ldc, hipStream_t stream);
+
+/*
+ * Expert products on 16-bit operands over ragged groups, and their gradients:
+ *   grouped_gemm        y[r, n]     = round(sum_k x[r, k] * w[e, n, k])
+ *   grouped_gemm_dgrad  dx[r, k]    = round(sum_n dy[r, n] * w[e, n, k])
+ *   grouped_gemm_wgrad  dw[e, n, k] = round(sum_{r of expert e} dy[r, n] * x[r, k])
+ * x [R, K], dy [R, N], y [R, N], dx [R, K]: bf16 bits, or fp16 bits when fp16 is 1, row
+ * strides ld_*; w [E, N, K] contiguous, the same type; dw [E, N, K] the same type, or fp32 when
+ * out_fp32 is 1.  fp32 sums, rounded once.  An expert without rows gets a dw of zeros.
+ * Infinities and NaN stay in the rows (wgrad: the expert) that hold them.
+ * N % 8 == 0, K % 8 == 0, row strides up to 2097152 elements, E < 65536, else
+ * MOE355_EUNSUPPORTED; pointers 16-byte aligned and strides multiples of 8, else
+ * MOE355_EMISALIGNED.
+ */
+int grouped_gemm(const uint16_t* x, int fp16, int64_t ld_x, const uint16_t* w, const int32_t* offsets,
+                 int R, int E, int N, int K, uint16_t* y, int64_t ld_y, hipStream_t stream);
+int grouped_gemm_dgrad(const uint16_t* dy, int fp16, int64_t ld_dy, const uint16_t* w,
+                       const int32_t* offsets, int R, int E, int N, int K, uint16_t* dx, int64_t ld_dx,
+                       hipStream_t stream);
+int grouped_gemm_wgrad(const uint16_t* dy, int fp16, int64_t ld_dy, const uint16_t* x, int64_t ld_x,
+                       const int32_t* offsets, int R, int E, int N, int K, void* dw, int out_fp32,
+                       hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
