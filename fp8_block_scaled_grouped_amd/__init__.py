@@ -12,6 +12,7 @@ from .moe355 import (  # noqa: F401
     fp4_quant_groups,
     fp8_quant_1x128,
     gemm_fp4_groupscale,
+    gemm_fp4_groupscale_workspace,
     gemm_fp8_blockscale,
     gemm_fp8_blockscale_plan,
     gemm_fp8_blockscale_tiled,

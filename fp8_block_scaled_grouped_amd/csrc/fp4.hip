@@ -16,6 +16,7 @@ namespace moe355 {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int64_t kMaxLd = 1 << 21;  // a pass's rows stay within 2^31 bytes
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 template <bool F16>
@@ -159,19 +160,29 @@ extern "C" int fp4_dequant_groups(const uint8_t* q, const void* scale, int e8m0,
   return launch_status();
 }
 
+extern "C" int gemm_fp4_groupscale_workspace(int M, int N, int K, size_t* bytes) {
+  MOE355_CHECK(M >= 0 && N >= 0 && K >= 0 && bytes, MOE355_EINVAL);
+  MOE355_CHECK(K % 32 == 0, MOE355_EUNSUPPORTED);
+  const int splits = M && N && K ? skinny_splits(M, N, K) : 1;
+  *bytes = splits > 1 ? (size_t)splits * M * N * sizeof(float) : 0;
+  return MOE355_OK;
+}
+
 extern "C" int gemm_fp4_groupscale(const uint16_t* x, int fp16, int64_t ld_x, const uint8_t* q, const void* scale,
-                                   int e8m0, int group, int M, int N, int K, uint16_t* c, int64_t ldc,
-                                   hipStream_t stream) {
+                                   int e8m0, int group, int M, int N, int K, uint16_t* c, int64_t ldc, void* workspace,
+                                   size_t workspace_bytes, hipStream_t stream) {
   if (int st = check_format(fp16, group, e8m0)) return st;
   MOE355_CHECK(M >= 0 && N >= 0 && K >= 0 && ld_x >= K && ldc >= N, MOE355_EINVAL);
-  MOE355_CHECK(K % 32 == 0, MOE355_EUNSUPPORTED);
+  MOE355_CHECK(K % 32 == 0 && ld_x <= kMaxLd, MOE355_EUNSUPPORTED);
   if (M == 0 || N == 0) return MOE355_OK;
   MOE355_CHECK(c && (K == 0 || (x && q && scale)), MOE355_EINVAL);
   MOE355_CHECK((K == 0 || (aligned16(x) && ld_x % 8 == 0 && aligned16(q) && aligned_scale(scale, e8m0))) &&
-                   (reinterpret_cast<uintptr_t>(c) & 1u) == 0,
+                   (reinterpret_cast<uintptr_t>(c) & 1u) == 0 && aligned16(workspace),
                MOE355_EMISALIGNED);
-  return launch_skinny(SkinnyArgs{x, q, scale, nullptr, c, ld_x, ldc, M, 1, N, K}, e8m0 ? kFp4E8M0 : kFp4, group, fp16,
-                       stream);
+  const int splits = workspace && K ? skinny_splits(M, N, K) : 1;
+  MOE355_CHECK(splits == 1 || workspace_bytes >= (size_t)splits * M * N * sizeof(float), MOE355_EINVAL);
+  return launch_skinny(SkinnyArgs{x, q, scale, nullptr, c, ld_x, ldc, M, 1, N, K, splits, static_cast<float*>(workspace)},
+                       e8m0 ? kFp4E8M0 : kFp4, group, fp16, stream);
 }
 
 extern "C" int grouped_gemm_fp4(const uint16_t* x, int fp16, int64_t ld_x, const uint8_t* q, const void* scale,
@@ -179,12 +190,12 @@ extern "C" int grouped_gemm_fp4(const uint16_t* x, int fp16, int64_t ld_x, const
                                 int64_t ldc, hipStream_t stream) {
   if (int st = check_format(fp16, group, e8m0)) return st;
   MOE355_CHECK(R >= 0 && E >= 0 && N >= 0 && K >= 0 && ld_x >= K && ldc >= N, MOE355_EINVAL);
-  MOE355_CHECK(K % 32 == 0 && E < 65536, MOE355_EUNSUPPORTED);
+  MOE355_CHECK(K % 32 == 0 && E < 65536 && ld_x <= kMaxLd, MOE355_EUNSUPPORTED);
   if (R == 0 || E == 0 || N == 0) return MOE355_OK;
   MOE355_CHECK(offsets && c && (K == 0 || (x && q && scale)), MOE355_EINVAL);
   MOE355_CHECK((K == 0 || (aligned16(x) && ld_x % 8 == 0 && aligned16(q) && aligned_scale(scale, e8m0))) &&
                    (reinterpret_cast<uintptr_t>(c) & 1u) == 0 && (reinterpret_cast<uintptr_t>(offsets) & 3u) == 0,
                MOE355_EMISALIGNED);
-  return launch_skinny(SkinnyArgs{x, q, scale, offsets, c, ld_x, ldc, R, E, N, K}, e8m0 ? kFp4E8M0 : kFp4, group, fp16,
+  return launch_skinny(SkinnyArgs{x, q, scale, offsets, c, ld_x, ldc, R, E, N, K, 1, nullptr}, e8m0 ? kFp4E8M0 : kFp4, group, fp16,
                        stream);
 }

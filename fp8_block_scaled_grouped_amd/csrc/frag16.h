@@ -44,9 +44,28 @@ __device__ __forceinline__ s16x8 e2m1x8(uint32_t codes, float scale) {
   return __builtin_bit_cast(s16x8, r);
 }
 
-// fp32 value of an E8M0 scale code: 2^(code - 127), NaN for 255
+constexpr uint32_t kPastEnd = 0x80000000u;  // a lane offset beyond every descriptor's length
+
+// Buffer descriptor of at most 2^31 - 16 bytes for dma16_buf; lane offsets from `bytes` on read zeros.
+__device__ __forceinline__ u32x4 dma_buffer(const void* base, int64_t bytes) {
+  const uint64_t v = reinterpret_cast<uint64_t>(base);
+  return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)v),
+               (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(v >> 32)) & 0xffffu,
+               (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)min(bytes, (int64_t)0x7ffffff0)), 0x00020000u};
+}
+
+// LDS-DMA through a buffer descriptor: lane l moves 16 bytes from base + off to
+// LDS[m0 + 16 l]; off at or past the descriptor's length writes zeros.  Completion is
+// counted with vm_wait.
+__device__ __forceinline__ void dma16_buf(u32x4 rsrc, uint32_t off, uint32_t m0) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(off), "s"(rsrc), "s"(m0)
+               : "memory");
+}
+
+// fp32 value of an E8M0 scale code, 2^(code - 127) or NaN for 255: the conversion of the e4m3
+// code of 1.0 under that scale, which also gets the subnormal 2^-127 right.
 __device__ __forceinline__ float e8m0_to_f32(uint32_t code) {
-  return __uint_as_float(code == 0 ? 0x00400000u : code == 255u ? 0x7fc00000u : code << 23);
+  return __builtin_amdgcn_cvt_scalef32_f32_fp8(0x38, __uint_as_float(code << 23), 0);
 }
 
 // Segment [lo, hi) of expert e, kept inside [0, R] whatever the offsets hold.

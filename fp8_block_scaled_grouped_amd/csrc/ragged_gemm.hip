@@ -25,22 +25,6 @@ namespace moe355 {
 namespace {
 
 constexpr int kBK = 64;                      // k per step
-constexpr uint32_t kPastEnd = 0x80000000u;   // a lane offset beyond every descriptor's length
-
-// LDS-DMA through a buffer descriptor: lane l moves 16 bytes from base + off to
-// LDS[m0 + 16 l]; off at or past the descriptor's length writes zeros.
-__device__ __forceinline__ void dma16_buf(u32x4 rsrc, uint32_t off, uint32_t m0) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(off), "s"(rsrc), "s"(m0)
-               : "memory");
-}
-
-__device__ __forceinline__ u32x4 buffer_of(const void* base, uint32_t bytes) {
-  const uint64_t v = reinterpret_cast<uint64_t>(base);
-  return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)v),
-               (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(v >> 32)) & 0xffffu,
-               (uint32_t)__builtin_amdgcn_readfirstlane(bytes), 0x00020000u};
-}
-
 // Rotation of the 32-byte column pairs of k-row r in a tile read transposed: the 8 k-rows
 // that half a wave touches in one read land in different banks.
 __device__ __forceinline__ int tr_swz(int r) { return (r & 3) | ((r >> 1) & 4); }
@@ -234,8 +218,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void ragged_gemm_kernel(RaggedArgs
   auto fetch = [&](uint32_t stage) {  // DMAs of the next step into a stage; past the last step none
     if (fetched < steps) {
       const int krem = kdim - fetched * kBK;
-      oa.fetch(buffer_of(pa, (uint32_t)min(lena * 2, (int64_t)0x7ffffff0)), stage, w, krem);
-      ob.fetch(buffer_of(pb, (uint32_t)min(lenb * 2, (int64_t)0x7ffffff0)), stage + OA::kBytes, w, krem);
+      oa.fetch(dma_buffer(pa, lena * 2), stage, w, krem);
+      ob.fetch(dma_buffer(pb, lenb * 2), stage + OA::kBytes, w, krem);
       pa += stepa;
       pb += stepb;
       lena -= stepa;

@@ -3,28 +3,39 @@
 //
 //   4-bit: c[m, n] = round(sum_g s[n, g] sum_{k in group g} x[m, k] q[n, k])
 //
-// The weights are read once and nothing of them is reused, so they go from memory straight
-// into MFMA operands: 16 weight rows are the product's columns, up to 16 MT rows of x its
-// rows.  A wave walks a run of 128-wide k blocks; the KW waves that share columns add their
-// fp32 tiles in LDS in wave order (one launch, no workspace, deterministic).
+// The weights are read once and bound the time, so the kernel is built around their stream:
+// one wave of a workgroup does nothing but LDS-DMA, S stages deep, in whole 128-byte lines of
+// the weight rows (fragment-shaped loads straight into registers, 16 rows x 64 bytes each,
+// ask for twice as many lines and the requests in flight, not the bytes, bounded them).  The
+// other waves multiply from LDS: 16 weight rows are an MFMA's columns, 16 rows of x its rows.  A
+// stage is 128 H k for each of KW waves that share columns; they add their fp32 tiles in LDS in
+// wave order at the end (deterministic, one launch, no workspace).
 //
-// A lane loads 16 bytes of a weight row's block: 32 codes, k [32 g, 32 g + 32) for lane group g
-// = lane / 16.  The conversion instruction turns 8 codes into an operand in 4 issues.  E8M0
-// scales with bf16 x go into the conversion itself (exact).  Else the scale multiplies the
-// fp32 tile of its group, so an MFMA's 32 k must lie in one group: groups of 128 take any
-// order, for groups of 64 and 32 the lanes of a column exchange codes first (one or two
-// lane-swap steps), and x is read in the order that results.
+// A lane takes 16 bytes of a weight row's 128-wide block: 32 codes, k [32 g, 32 g + 32) for
+// lane group g = lane / 16.  The conversion instruction turns 8 codes into an operand in 4
+// issues.  E8M0 scales with bf16 x go into the conversion itself (exact).  Else the scale
+// multiplies the fp32 tile of its group, so an MFMA's 32 k must lie in one group: groups of
+// 128 take any order, for groups of 64 and 32 the lanes of a column exchange codes first (one
+// or two lane-swap steps), and x is read in the order that results.
+//
+// Columns past N, rows past the segment and k past K lie past the end of the buffer
+// descriptors: they arrive as zeros, without traffic.
+//
+// Measured (18432 x 7168, fp32 scales of 128): 1 row 15.5 us (4.5 TB/s of weights and scales;
+// fragment-shaped register loads 31 us), 16 rows 22 us; 64 tokens through 222 of 256 experts of
+// 7168 x 2048 302 us (5.8 TB/s; 497 us).  A single copying wave issues too slowly for a CU's share
+// of the stream: with two, 1 row over 2048 x 7168 takes 6.8 us instead of 8.4, with 64 rows four
+// take 33 us where one takes 46.
 #include "skinny.h"
 
 #include <type_traits>
 
 #include "frag16.h"
+#include "gemm_engine.h"
 #include "host_common.h"
 
 namespace moe355 {
 namespace {
-
-constexpr int kWaves = 8;
 
 // vdst's upper 32 lanes <-> vsrc's lower 32 lanes
 __device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b) {
@@ -39,178 +50,379 @@ __device__ __forceinline__ void swap16(uint32_t& a, uint32_t& b) {
   b = r[1];
 }
 
-template <int W, int GROUP, bool F16>
-struct Weights {
-  static constexpr bool kDirect = W == kFp4E8M0 && !F16;             // scale inside the conversion
-  static constexpr int kLoads = W == kW16 ? 4 : 1;                   // 16-byte loads of a row's block per lane
-  static constexpr int kScales = W == kW16 ? 0 : kDirect ? 1 : 128 / GROUP;
-  static constexpr int kPerScale = W == kW16 || kDirect ? 4 : GROUP / 32;  // MFMAs that share a fold
+// LDS-DMA of a dword per lane.
+__device__ __forceinline__ void dma4_buf(u32x4 rsrc, uint32_t off, uint32_t m0) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds" ::"v"(off), "s"(rsrc), "s"(m0)
+               : "memory");
+}
 
-  u32x4 q[kLoads];
-  float s[kScales ? kScales : 1];
+// LDS-DMA of COUNT KB as rows of RC 16-byte chunks, chunk c of row r in slot c ^ (r & MASK).
+template <int COUNT, int RC, int MASK>
+struct RowCopy {
+  static constexpr int kRows = RC < 64 ? 64 / RC : 1;   // rows of a DMA instruction
+  static constexpr int kParts = RC < 64 ? 1 : RC / 64;  // instructions of a row
+  uint32_t base;  // byte offset of the lane's first row
+  int chunk;      // its chunk in that row
 
-  // block kb of weight row `row`; lanes past K get zeros
-  __device__ __forceinline__ void load(const uint8_t* row, const void* scale, int64_t srow, int kb, int K, int G, int g) {
-    if constexpr (W == kW16) {
+  __device__ __forceinline__ void init(int lane, int64_t stride) {
+    const int r = RC < 64 ? lane / RC : 0;
+    base = (uint32_t)(r * stride);
+    chunk = (RC < 64 ? lane % RC : lane) ^ (r & MASK);
+  }
+  // TAIL: chunks of `left` and more read zeros;
+  // and only instructions `part`, part + PARTS, ... are this wave's.
+  template <bool TAIL, int PARTS>
+  __device__ __forceinline__ void copy(u32x4 rsrc, uint32_t dst, uint32_t stride, int left, int part) const {
+    // The offsets are the same in every stage; kept in registers they would take more of them than
+    // the multiplying waves have, so each call computes them (3 VALU a DMA) from values that the
+    // compiler must take for new.
+    uint32_t base = this->base;
+    int chunk = this->chunk;
+    asm volatile("" : "+v"(base), "+v"(chunk));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int k = kb * 128 + 32 * i + 8 * g;
-        q[i] = k < K ? *reinterpret_cast<const u32x4*>(row + 2 * (int64_t)k) : u32x4{0, 0, 0, 0};
-      }
-    } else {
-      const int k = kb * 128 + 32 * g;
-      q[0] = k < K ? __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(row + k / 2)) : u32x4{0, 0, 0, 0};
-#pragma unroll
-      for (int i = 0; i < kScales; ++i) {
-        const int at = kDirect ? (kb * 128 + 32 * g) / GROUP : kb * (128 / GROUP) + i;
-        const int in = min(at, G - 1);
-        if constexpr (W == kFp4) {
-          s[i] = reinterpret_cast<const float*>(scale)[srow + in];
-        } else {
-          const uint32_t c = reinterpret_cast<const uint8_t*>(scale)[srow + in];
-          // the conversion reads the exponent field (0 as 2^-127)
-          s[i] = kDirect ? __uint_as_float(c << 23) : e8m0_to_f32(c);
-        }
-      }
+    for (int i = 0; i < COUNT / PARTS; ++i) {
+      const int j = i * PARTS + part, row = j / kParts * kRows, c = (chunk ^ (row & MASK)) + j % kParts * 64;
+      const uint32_t off = base + row * stride + c * 16;
+      dma16_buf(rsrc, TAIL && c >= left ? kPastEnd : off, dst + j * 1024);
     }
   }
+};
+
+template <int W, int GROUP, bool F16>
+struct Format {
+  static constexpr bool kDirect = W == kFp4E8M0 && !F16;    // scale inside the conversion
+  static constexpr bool kFold = W != kW16 && !kDirect;      // scale on the fp32 tile
+  static constexpr int kChunks = W == kW16 ? 16 : 4;        // 16-byte chunks of a row's 128-wide block
+  static constexpr int kPerChunk = W == kW16 ? 8 : 32;      // k of a chunk
+  static constexpr int kLoads = W == kW16 ? 4 : 1;          // chunks a lane reads per 128-wide block
+  static constexpr int kPerScale = kFold ? GROUP / 32 : 4;  // MFMAs that share a fold
+  static constexpr int kFolds = 4 / kPerScale;              // folds of a block
+  static constexpr int kScaleBytes = W == kFp4 ? 4 : 1;
+
   // 8-wide chunk of x's block that goes with operand i of lane group g
-  static __device__ __forceinline__ int chunk(int i, int g) {
-    if constexpr (W == kW16 || (!kDirect && GROUP == 32)) return 4 * i + g;
-    if constexpr (!kDirect && GROUP == 64) return 8 * (i >> 1) + (i & 1) + 4 * (g & 1) + 2 * (g >> 1);
+  static __device__ __forceinline__ int xchunk(int i, int g) {
+    if constexpr (W == kW16 || (kFold && GROUP == 32)) return 4 * i + g;
+    if constexpr (kFold && GROUP == 64) return 8 * (i >> 1) + (i & 1) + 4 * (g & 1) + 2 * (g >> 1);
     return 4 * g + i;
   }
-  __device__ __forceinline__ void arrange() {
-    if constexpr (W != kW16 && !kDirect && GROUP <= 64) {
-      uint32_t d[4] = {q[0][0], q[0][1], q[0][2], q[0][3]};
+  static __device__ __forceinline__ void arrange(u32x4& q) {
+    if constexpr (kFold && GROUP <= 64) {
+      uint32_t d[4] = {q[0], q[1], q[2], q[3]};
       swap32(d[0], d[2]);
       swap32(d[1], d[3]);
       if constexpr (GROUP == 32) {
         swap16(d[0], d[1]);
         swap16(d[2], d[3]);
       }
-      q[0] = u32x4{d[0], d[1], d[2], d[3]};
+      q = u32x4{d[0], d[1], d[2], d[3]};
     }
-  }
-  __device__ __forceinline__ s16x8 operand(int i) const {
-    if constexpr (W == kW16) return __builtin_bit_cast(s16x8, q[i]);
-    return e2m1x8<F16>(q[0][i], kDirect ? s[0] : 1.0f);
   }
 };
 
-template <int W, int GROUP, bool F16, int MT, int CW>
-__global__ __launch_bounds__(kWaves * 64) void skinny_kernel(SkinnyArgs a) {
-  using Wt = Weights<W, GROUP, F16>;
-  constexpr int KW = kWaves / CW;
-  constexpr int kDepth = W == kW16 || MT >= 4 ? 2 : 4;  // blocks of weights in flight per wave
-  __shared__ v4f part[kWaves][MT][64];
+// MR: rows of x per pass; CT: 16-column tiles per wave; CW x KW multiplying waves; H: 128-wide blocks
+// of a wave in a stage; S: stages; NP: copying waves.
+template <int W, int GROUP, bool F16, int MR, int CT, int CW, int KW, int H, int S, int NP>
+struct Skinny {
+  using Fm = Format<W, GROUP, F16>;
+  static constexpr int MT = MR > 16 ? MR / 16 : 1;
+  static constexpr int NW = CW * KW, NC = 16 * CT * CW;
+  static constexpr int kK = 128 * H * KW;                       // k of a stage
+  static constexpr int kRowChunks = KW * H * Fm::kChunks;       // of a weight row in a stage
+  static constexpr int kWMask = kRowChunks < 16 ? kRowChunks - 1 : 15;  // of the weights' swizzle
+  static constexpr int kWBytes = NC * kRowChunks * 16;          // weights of a stage
+  static constexpr int kXBytes = MR * kK * 2;
+  static constexpr int kStage = kWBytes + kXBytes;
+  static constexpr int kDmaW = kWBytes / 1024, kDmaX = kXBytes / 1024;
+  static constexpr int kInFlight = (S - 2) * (kDmaW + kDmaX) / NP > 63 ? 63 : (S - 2) * (kDmaW + kDmaX) / NP;
+  static constexpr int kPart = NW * MT * CT * 1024;
+  static constexpr int kWindowStages = 2048 / kK > 4 ? 2048 / kK : 4;  // stages of a window of scales
+  static constexpr int kSpan = kWindowStages * kK;                     // and its k
+  static constexpr int kWindow = kSpan / GROUP;                        // and its scales of a row
+  static_assert(kWindowStages >= S, "a window of scales outlives the stages in flight");
+  static_assert(kDmaW % NP == 0 && kDmaX % NP == 0, "the copying waves share the DMAs evenly");
+  static_assert(kWBytes % 1024 == 0 && kXBytes % 1024 == 0, "whole DMAs");
+  static int stages(int K) { return (K + kK - 1) / kK; }
+  // slots of a row in a window: a power of two that holds the row's scales or kWindow of them
+  static int scale_slots(int K) {
+    const int need = (K > kSpan ? kSpan : stages(K) * kK) / GROUP;
+    int n = 4;
+    while (n < need) n *= 2;
+    return n;
+  }
+  // two windows when a row has more than one
+  static int lds_bytes(int K) {
+    const int scales = W == kW16 ? 0 : (K > kSpan ? 2 : 1) * NC * scale_slots(K) * Fm::kScaleBytes;
+    const int run = S * kStage + scales;
+    return run > kPart ? run : kPart;
+  }
+};
+
+// slots: scales of a row in a window (a power of two); loose: E8M0 rows that do not start on dwords
+// (their scales are read from memory where they are used).
+template <int W, int GROUP, bool F16, int MR, int CT, int CW, int KW, int H, int S, int NP>
+__global__ __launch_bounds__((CW * KW + NP) * 64) void skinny_kernel(SkinnyArgs a, int slots, int loose) {
+  using Sk = Skinny<W, GROUP, F16, MR, CT, CW, KW, H, S, NP>;
+  using Fm = typename Sk::Fm;
+  constexpr int MT = Sk::MT, NW = Sk::NW;
+  extern __shared__ __align__(16) uint8_t smem[];  // stages, windows of scales; at the end the waves' tiles
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int cw = w / KW, kw = w % KW;
-  const int e = blockIdx.y;
+  const int e = blockIdx.y, n0 = blockIdx.x * Sk::NC;
   int lo = 0, hi = a.R;
   if (a.offsets) segment(a.offsets, a.R, e, lo, hi);
+  lo = __builtin_amdgcn_readfirstlane(lo);
+  hi = __builtin_amdgcn_readfirstlane(hi);
   if (lo == hi) return;
-  const int n0 = (blockIdx.x * CW + cw) * 16;
+  // this workgroup's stages: all, or one of `splits` runs of them
+  const int all = (a.K + Sk::kK - 1) / Sk::kK, per = (all + a.splits - 1) / a.splits;
+  const int split = blockIdx.z % a.splits, s0 = min(all, split * per), s1 = min(all, s0 + per);
+  const int zrow = blockIdx.z / a.splits, zrows = gridDim.z / a.splits;
+  const int G = W == kW16 ? 0 : (a.K + GROUP - 1) / GROUP;
+  const int64_t srowbytes = (int64_t)G * Fm::kScaleBytes;
+  const uint8_t* scales = reinterpret_cast<const uint8_t*>(a.scale) + ((int64_t)e * a.N + n0) * srowbytes;
+  const int cols = min(a.N - n0, Sk::NC);
+  const uint32_t lds0 = lds_addr(smem), lds_scale = lds0 + S * Sk::kStage;
+  const uint32_t window = Sk::NC * slots * Fm::kScaleBytes;  // bytes
 
-  const int KB = (a.K + 127) / 128, G = W == kW16 ? 0 : (a.K + GROUP - 1) / GROUP;
-  const int per = (KB + KW - 1) / KW;
-  const int kb0 = min(KB, kw * per), kb1 = min(KB, kb0 + per);
-  // weight row of this lane (rows past N repeat row N - 1: in bounds, results not stored)
-  const int64_t wr = (int64_t)e * a.N + min(n0 + (lane & 15), a.N - 1);
-  const uint8_t* row = a.w + wr * (W == kW16 ? 2 * (int64_t)a.K : (int64_t)a.K / 2);
-  const int64_t srow = wr * G;
-
-  const int mstep = gridDim.z * 16 * MT;
-  for (int m0 = lo + blockIdx.z * 16 * MT; m0 < hi; m0 += mstep) {
-    const uint16_t* xrow[MT];
-#pragma unroll
-    for (int t = 0; t < MT; ++t) xrow[t] = a.x + (int64_t)min(m0 + 16 * t + (lane & 15), hi - 1) * a.ldx;
-    v4f acc[MT];
-#pragma unroll
-    for (int t = 0; t < MT; ++t) acc[t] = v4f{0.f, 0.f, 0.f, 0.f};
-    Wt wq[kDepth];
-    s16x8 xq[MT][4];
-    auto load_x = [&](int kb) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int k = kb * 128 + 8 * Wt::chunk(i, g);
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-          xq[t][i] = k < a.K ? *reinterpret_cast<const s16x8*>(xrow[t] + k) : s16x8{0, 0, 0, 0, 0, 0, 0, 0};
-      }
-    };
-#pragma unroll
-    for (int d = 0; d < kDepth; ++d)
-      if (kb0 + d < kb1) wq[d].load(row, a.scale, srow, kb0 + d, a.K, G, g);
-    if (kb0 < kb1) load_x(kb0);
-    for (int kb = kb0; kb < kb1; kb += kDepth) {
-#pragma unroll
-      for (int d = 0; d < kDepth; ++d) {
-        if (kb + d < kb1) {
-          Wt now = wq[d];
-          if (kb + d + kDepth < kb1) wq[d].load(row, a.scale, srow, kb + d + kDepth, a.K, G, g);
-          s16x8 xn[MT][4];
-#pragma unroll
-          for (int t = 0; t < MT; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) xn[t][i] = xq[t][i];
-          if (kb + d + 1 < kb1) load_x(kb + d + 1);
-          now.arrange();
-          v4f tile[MT];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const s16x8 b = now.operand(i);
-            const bool first = i % Wt::kPerScale == 0, last = i % Wt::kPerScale == Wt::kPerScale - 1;
-#pragma unroll
-            for (int t = 0; t < MT; ++t) {
-              if constexpr (Wt::kScales == 0 || Wt::kDirect) {
-                acc[t] = mfma16x16x32<F16>(xn[t][i], b, acc[t]);
-              } else {
-                tile[t] = mfma16x16x32<F16>(xn[t][i], b, first ? v4f{0.f, 0.f, 0.f, 0.f} : tile[t]);
-                if (last) acc[t] += tile[t] * now.s[i / Wt::kPerScale];
-              }
+  for (int m0 = lo + zrow * MR; m0 < hi; m0 += zrows * MR) {
+    if (w >= NW) {
+      const int part = w - NW;
+      const int64_t rowbytes = (int64_t)a.K * 16 / Fm::kPerChunk;
+      const int rows = min(hi - m0, MR);
+      const uint8_t* wp = a.w + ((int64_t)e * a.N + n0) * rowbytes + (int64_t)s0 * Sk::kRowChunks * 16;
+      const uint8_t* xp = reinterpret_cast<const uint8_t*>(a.x + (int64_t)m0 * a.ldx) + (int64_t)s0 * Sk::kK * 2;
+      int64_t wlen = cols * rowbytes - (int64_t)s0 * Sk::kRowChunks * 16;
+      int64_t xlen = ((int64_t)(rows - 1) * a.ldx + a.K) * 2 - (int64_t)s0 * Sk::kK * 2;
+      RowCopy<Sk::kDmaW, Sk::kRowChunks, Sk::kWMask> wc;
+      RowCopy<Sk::kDmaX, Sk::kK / 8, 15> xc;
+      wc.init(lane, rowbytes);
+      xc.init(lane, a.ldx * 2);
+      auto fetch = [&](int s) {
+        if (s >= s1) return;
+        const uint32_t dst = lds0 + (s % S) * Sk::kStage;
+        const u32x4 wd = dma_buffer(wp, wlen), xd = dma_buffer(xp, xlen);
+        const int left = a.K - s * Sk::kK;
+        if (left >= Sk::kK) {
+          wc.template copy<false, NP>(wd, dst, (uint32_t)rowbytes, 0, part);
+          xc.template copy<false, NP>(xd, dst + Sk::kWBytes, (uint32_t)a.ldx * 2, 0, part);
+        } else {
+          wc.template copy<true, NP>(wd, dst, (uint32_t)rowbytes, (left + Fm::kPerChunk - 1) / Fm::kPerChunk, part);
+          xc.template copy<true, NP>(xd, dst + Sk::kWBytes, (uint32_t)a.ldx * 2, left / 8, part);
+        }
+        if constexpr (W != kW16) {
+          if ((s == s0 || s % Sk::kWindowStages == 0) && !loose) {
+            // dword i of the window: row i / (dwords of a row); dwords past the row's end are zeros
+            const int q = s / Sk::kWindowStages, sh = 31 - __builtin_clz(slots * Fm::kScaleBytes / 4);
+            const int first = q * Sk::kWindow * Fm::kScaleBytes;
+            const u32x4 sd = dma_buffer(scales, cols * srowbytes);
+            const uint32_t win = lds_scale + (q & 1) * window;
+            for (int i0 = 64 * part; i0 < (Sk::NC << sh); i0 += 64 * NP) {
+              const int i = i0 + lane, r = i >> sh, at = first + (i - (r << sh)) * 4;
+              if (i < Sk::NC << sh)
+                dma4_buf(sd, at < srowbytes ? (uint32_t)r * (uint32_t)srowbytes + at : kPastEnd, win + i0 * 4);
             }
           }
         }
+        wp += Sk::kRowChunks * 16;
+        xp += Sk::kK * 2;
+        wlen -= Sk::kRowChunks * 16;
+        xlen -= Sk::kK * 2;
+      };
+#pragma unroll 1
+      for (int s = s0; s < s0 + S - 1; ++s) fetch(s);
+#pragma unroll 1
+      for (int s = s0; s < s1; ++s) {
+        // stage s has landed when only the S - 2 stages after it are in flight
+        if (s + S - 1 <= s1) {
+          vm_wait<Sk::kInFlight>();
+        } else {
+          vm_wait<0>();
+        }
+        barrier_only();  // stage s is there; stage s - 1 has been read
+        fetch(s + S - 1);
       }
+      barrier_only();
+    } else {
+      const int cw = w / KW, kw = w % KW, r = lane & 15;
+      // weights: row r of a tile, chunk (kw, block, g); x: row r, chunk (kw, block, operand)
+      uint32_t wat[H][Fm::kLoads], xat[4];
+#pragma unroll
+      for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int i = 0; i < Fm::kLoads; ++i)
+          wat[h][i] = (cw * CT * 16 + r) * (Sk::kRowChunks * 16) +
+                      ((((kw * H + h) * Fm::kChunks + 4 * i + g) ^ (r & Sk::kWMask)) << 4);
+      const int xr = r & (MR < 16 ? MR - 1 : 15);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        xat[i] = Sk::kWBytes + xr * (Sk::kK * 2) + ((kw * H * 16 + (Fm::xchunk(i, g) ^ (xr & 15))) << 4);
+      // the lane's column, the wave's first group of a stage; E8M0 in the conversion: the lane's own group
+      const int col = cw * CT * 16 + r;
+      const int sgroup = kw * H * 128 / GROUP + (Fm::kDirect ? 32 * g / GROUP : 0);
+
+      v4f acc[MT][CT];
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int c = 0; c < CT; ++c) acc[t][c] = v4f{0.f, 0.f, 0.f, 0.f};
+      typedef __attribute__((address_space(3))) const u32x4* pv;
+      typedef __attribute__((address_space(3))) const s16x8* px;
+      typedef __attribute__((address_space(3))) const uint32_t* pu;
+      typedef __attribute__((address_space(3))) const uint8_t* pb;
+
+#pragma unroll 1
+      for (int s = s0; s < s1; ++s) {
+        barrier_only();
+        const uint32_t st = lds0 + (s % S) * Sk::kStage;
+        const uint32_t win = lds_scale + (s / Sk::kWindowStages & 1) * window;
+        const int sw = s % Sk::kWindowStages * (Sk::kK / GROUP) + sgroup;  // slot in the window
+        auto scale_of = [&](int c, int at) -> uint32_t {                   // of tile c, group `at` on from sgroup
+          const int row = col + 16 * c;
+          if constexpr (W == kFp4) {
+            return *reinterpret_cast<pu>(win + (row * slots + sw + at) * 4);
+          } else {
+            if (loose) return scales[min(row, cols - 1) * srowbytes + min(s * (Sk::kK / GROUP) + sgroup + at, G - 1)];
+            return *reinterpret_cast<pb>(win + row * slots + sw + at);
+          }
+        };
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+          s16x8 x[MT][4];
+#pragma unroll
+          for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[t][i] = *reinterpret_cast<px>(st + xat[i] + h * 256 + t * 16 * (Sk::kK * 2));
+#pragma unroll
+          for (int c = 0; c < CT; ++c) {
+            u32x4 q[Fm::kLoads];
+#pragma unroll
+            for (int i = 0; i < Fm::kLoads; ++i)
+              q[i] = *reinterpret_cast<pv>(st + wat[h][i] + c * 16 * (Sk::kRowChunks * 16));
+            uint32_t sv[Fm::kFolds];
+            if constexpr (W != kW16) {
+#pragma unroll
+              for (int i = 0; i < Fm::kFolds; ++i) sv[i] = scale_of(c, h * (128 / GROUP) + i);
+              Fm::arrange(q[0]);
+            }
+            v4f tile[MT];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              s16x8 b;
+              if constexpr (W == kW16) {
+                const u32x4 v = q[i];
+                b = __builtin_bit_cast(s16x8, v);
+              } else {  // the conversion reads the scale's exponent field (0 as 2^-127)
+                b = e2m1x8<F16>(q[0][i], Fm::kDirect ? __uint_as_float(sv[0] << 23) : 1.0f);
+              }
+              const bool first = i % Fm::kPerScale == 0, last = i % Fm::kPerScale == Fm::kPerScale - 1;
+#pragma unroll
+              for (int t = 0; t < MT; ++t) {
+                if constexpr (!Fm::kFold) {
+                  acc[t][c] = mfma16x16x32<F16>(x[t][i], b, acc[t][c]);
+                } else {
+                  tile[t] = mfma16x16x32<F16>(x[t][i], b, first ? v4f{0.f, 0.f, 0.f, 0.f} : tile[t]);
+                  if (last) {
+                    const uint32_t u = sv[i / Fm::kPerScale];
+                    acc[t][c] += tile[t] * (W == kFp4 ? __uint_as_float(u) : e8m0_to_f32(u));
+                  }
+                }
+              }
+            }
+            if constexpr (Fm::kFold && MT * CT >= 8) __builtin_amdgcn_sched_barrier(0);  // and of one tile
+          }
+          __builtin_amdgcn_sched_barrier(0);  // keeps the operands of one block in registers at a time
+        }
+      }
+      barrier_only();  // every stage has been read: the tiles may overwrite them
+      v4f* part = reinterpret_cast<v4f*>(smem);
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int c = 0; c < CT; ++c) part[((w * MT + t) * CT + c) * 64 + lane] = acc[t][c];
     }
-#pragma unroll
-    for (int t = 0; t < MT; ++t) part[w][t][lane] = acc[t];
     __syncthreads();
-    for (int j = tid; j < CW * MT * 64; j += kWaves * 64) {  // whole waves: lane stays
-      const int t = j / 64 % MT, c = j / 64 / MT;
-      v4f s = part[c * KW][t][lane];
+    const v4f* part = reinterpret_cast<const v4f*>(smem);
+    for (int j = w; j < CW * MT * CT; j += NW + NP) {
+      const int c = j % CT, t = j / CT % MT, cc = j / CT / MT;
+      v4f s = part[((cc * KW * MT + t) * CT + c) * 64 + lane];
 #pragma unroll
-      for (int k = 1; k < KW; ++k) s += part[c * KW + k][t][lane];
-      const int n = (blockIdx.x * CW + c) * 16 + (lane & 15);
+      for (int k = 1; k < KW; ++k) s += part[(((cc * KW + k) * MT + t) * CT + c) * 64 + lane];
+      const int n = n0 + (cc * CT + c) * 16 + (lane & 15);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int m = m0 + 16 * t + 4 * g + i;
-        if (m < hi && n < a.N) a.c[(int64_t)m * a.ldc + n] = (uint16_t)f32_to_out16(s[i], F16);
+        if (m >= hi || m >= m0 + MR || n >= a.N) continue;
+        if (a.splits > 1) {
+          a.part[((int64_t)split * a.R + m) * a.N + n] = s[i];
+        } else {
+          a.c[(int64_t)m * a.ldc + n] = (uint16_t)f32_to_out16(s[i], F16);
+        }
       }
     }
     __syncthreads();
   }
 }
 
+// c = rounded sum of the splits' partial sums, in split order.
+template <bool F16>
+__global__ __launch_bounds__(256) void skinny_reduce_kernel(SkinnyArgs a) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, count = (int64_t)a.R * a.N;
+  if (i >= count) return;
+  float s = a.part[i];
+  for (int k = 1; k < a.splits; ++k) s += a.part[k * count + i];
+  const int64_t m = i / a.N;
+  a.c[m * a.ldc + (i - m * a.N)] = (uint16_t)f32_to_out16(s, F16);
+}
+
+template <int W, int GROUP, bool F16, int MR, int CT, int CW, int KW, int H, int S, int NP>
+int launch_tile(SkinnyArgs g, hipStream_t stream) {
+  using Sk = Skinny<W, GROUP, F16, MR, CT, CW, KW, H, S, NP>;
+  const int64_t nx = ceil_div64(g.N, Sk::NC), nz = (g.offsets ? 1 : ceil_div64(g.R, MR)) * g.splits;
+  MOE355_CHECK(nx < (1ll << 31) && nz < 65536, MOE355_EUNSUPPORTED);
+  auto* fn = &skinny_kernel<W, GROUP, F16, MR, CT, CW, KW, H, S, NP>;
+  const int lds = Sk::lds_bytes(g.K), G = (g.K + GROUP - 1) / GROUP;
+  const int loose = W == kFp4E8M0 && (G % 4 != 0 || (reinterpret_cast<uintptr_t>(g.scale) & 3u) != 0);
+  if (hipFuncSetAttribute(reinterpret_cast<const void*>(fn), hipFuncAttributeMaxDynamicSharedMemorySize, lds) !=
+      hipSuccess)
+    return MOE355_ELAUNCH;
+  hipLaunchKernelGGL(fn, dim3((unsigned)nx, (unsigned)g.E, (unsigned)nz), dim3((CW * KW + NP) * 64), lds, stream, g,
+                     Sk::scale_slots(g.K), loose);
+  if (g.splits > 1)
+    hipLaunchKernelGGL(skinny_reduce_kernel<F16>, dim3((unsigned)ceil_div64((int64_t)g.R * g.N, 256)), dim3(256), 0,
+                       stream, g);
+  return launch_status();
+}
+
 template <int W, int GROUP, bool F16>
 int launch(const SkinnyArgs& g, hipStream_t stream) {
+  constexpr int H = W == kW16 ? 1 : 2;  // 4-bit rows: whole 128-byte lines
+  constexpr int MR = W == kW16 ? 8 : 4;
   const int rows = g.offsets ? (int)ceil_div64(g.R, g.E) : g.R;  // of a matrix, on average
-  auto go = [&](auto mt, auto cw) {
-    constexpr int MT = decltype(mt)::value, CW = decltype(cw)::value;
-    const int64_t nx = ceil_div64(g.N, 16 * CW), nz = g.offsets ? 1 : ceil_div64(g.R, 16 * MT);
-    MOE355_CHECK(nx < (1ll << 31) && nz < 65536, MOE355_EUNSUPPORTED);
-    hipLaunchKernelGGL((skinny_kernel<W, GROUP, F16, MT, CW>), dim3((unsigned)nx, (unsigned)g.E, (unsigned)nz),
-                       dim3(kWaves * 64), 0, stream, g);
-    return launch_status();
-  };
-  const std::integral_constant<int, 1> one;
-  const std::integral_constant<int, 2> two;
-  const std::integral_constant<int, 4> four;
-  if (rows <= 16) return go(one, one);
-  if (rows <= 32) return go(two, two);
-  return go(four, two);
+  const int64_t mats = g.offsets && g.R < g.E ? g.R : g.E;       // with rows, at most
+  // Columns of a workgroup: 64 where that still makes two workgroups for every CU (then their K
+  // is walked by one wave: no tiles to add; 256 experts of 4096 x 7168, 512 rows: 591 us against 616
+  // with 32 columns), 16 where 32 would leave a quarter of the CUs idle (2048 x 7168, 1 row: 6.8
+  // against 9.4 us), else 32 (18432 x 7168, 1 row: 15.5 against 18.3 with 16 and 20.2 with 64).
+  const bool wide = ceil_div64(g.N, 64) * mats >= 512, narrow = ceil_div64(g.N, 32) * mats < 192;
+  // Rows of a pass: of an expert on average some have more, and then take another pass over
+  // weights that the caches still hold (512 rows over 256 experts of 7168 x 2048: 302 us with 4
+  // rows a pass, 366 with 16, whose empty rows cost DMAs).
+  if (rows <= (g.offsets ? 2 : 4)) {
+    if (wide) return launch_tile<W, GROUP, F16, MR, 1, 4, 1, H, 4, 2>(g, stream);
+    if (narrow) return launch_tile<W, GROUP, F16, MR, 1, 1, 4, H, 3, 2>(g, stream);
+    return launch_tile<W, GROUP, F16, MR, 1, 2, 2, H, 3, 2>(g, stream);
+  }
+  if (rows <= (g.offsets ? 12 : 16)) {
+    if (wide) return launch_tile<W, GROUP, F16, 16, 1, 4, 1, H, 4, 2>(g, stream);
+    if (narrow) return launch_tile<W, GROUP, F16, 16, 1, 1, 4, H, 3, 2>(g, stream);
+    return launch_tile<W, GROUP, F16, 16, 1, 2, 2, H, 3, 2>(g, stream);
+  }
+  if (rows <= 32) return launch_tile<W, GROUP, F16, 32, 2, 4, 1, H, 3, 2>(g, stream);
+  if constexpr (W == kW16 || (W == kFp4 && GROUP == 32)) {  // 256 columns' weights or scales do not fit
+    return launch_tile<W, GROUP, F16, 64, 2, 4, 1, 1, 3, 4>(g, stream);
+  } else {
+    return launch_tile<W, GROUP, F16, 64, 4, 4, 1, 1, 3, 4>(g, stream);
+  }
 }
 
 template <int W, bool F16>
@@ -223,6 +435,15 @@ int by_group(const SkinnyArgs& g, int group, hipStream_t stream) {
 }
 
 }  // namespace
+
+int skinny_splits(int M, int N, int K) {
+  if (M <= 32) return 1;
+  // 256 columns and 64 rows a workgroup, one workgroup a CU: as many runs of K as fill the 256
+  // CUs, of at least 8 stages of 128
+  const int64_t tiles = ceil_div64(N, 256) * ceil_div64(M, 64), runs = ceil_div64(K, 1024);
+  const int64_t s = tiles >= 256 ? 1 : 256 / tiles;
+  return (int)(s < runs ? s : runs);
+}
 
 int launch_skinny(const SkinnyArgs& g, int weights, int group, int fp16, hipStream_t stream) {
   if (weights == kW16) return fp16 ? launch<kW16, 128, true>(g, stream) : launch<kW16, 128, false>(g, stream);

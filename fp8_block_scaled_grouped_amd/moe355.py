@@ -46,7 +46,8 @@ _SIGNATURES = {
                                   _i32, _i32, _i64, _vp, _vp, _i64, _vp, _sz, _vp], _i32),
     "fp4_quant_groups": ([_vp, _i32, _i64, _i64, _i32, _i32, _vp, _vp, _i32, _vp], _i32),
     "fp4_dequant_groups": ([_vp, _vp, _i32, _i64, _i32, _i32, _vp, _i32, _i64, _vp], _i32),
-    "gemm_fp4_groupscale": ([_vp, _i32, _i64, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _i64, _vp], _i32),
+    "gemm_fp4_groupscale_workspace": ([_i32, _i32, _i32, _PSZ], _i32),
+    "gemm_fp4_groupscale": ([_vp, _i32, _i64, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _i64, _vp, _sz, _vp], _i32),
     "grouped_gemm_fp4": ([_vp, _i32, _i64, _vp, _vp, _i32, _i32, _vp, _i32, _i32, _i32, _i32, _vp, _i64, _vp], _i32),
     "grouped_gemm": ([_vp, _i32, _i64, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _i64, _vp], _i32),
     "grouped_gemm_dgrad": ([_vp, _i32, _i64, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _i64, _vp], _i32),
@@ -86,11 +87,12 @@ def _check(code):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    # the current stream's handle without a Stream object around it (2.7 us of a 12 us call)
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _dev(t, dtype, name):
@@ -104,7 +106,7 @@ def _dev(t, dtype, name):
 def _need(t, shape, dtype, name):
     """A contiguous device tensor of exactly this shape and dtype (the kernels index it densely)."""
     _dev(t, dtype, name)
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.shape != shape or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s tensor of shape %s, got %s" % (name, dtype, tuple(shape),
                                                                                  tuple(t.shape)))
     return t
@@ -463,9 +465,9 @@ def _half(t, name):
 def _out(t, shape, dtype, like, name):
     """The output tensor: allocated when None, else checked (2-D outputs may have strided rows)."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
     _dev(t, dtype, name)
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
     return t
 
@@ -524,21 +526,38 @@ def fp4_dequant_groups(q, scale, group=128, dtype=torch.bfloat16, out=None):
 
 def _ld(t, name):
     """Row stride of a 2-D tensor; of a single row (whose stride means nothing) its width."""
+    if t.dim() == 2 and t.is_contiguous():
+        return t.shape[1]
     ld = _rows(t, name)
     return ld if t.shape[0] > 1 else t.shape[1]
 
 
-def gemm_fp4_groupscale(x, q, scale, group=128, c=None):
+def gemm_fp4_groupscale_workspace(M, N, K):
+    """Bytes of partial sums with which gemm_fp4_groupscale splits K (host-only)."""
+    b = ctypes.c_size_t()
+    _check(lib().gemm_fp4_groupscale_workspace(M, N, K, ctypes.byref(b)))
+    return b.value
+
+
+def gemm_fp4_groupscale(x, q, scale, group=128, c=None, workspace=None):
     """x bf16 or fp16 [M, K] times 4-bit weights q [N, K/2] with scales [N, ceil(K/group)] (fp32, or
-    uint8 for E8M0), transposed: [M, N] in the type of x."""
+    uint8 for E8M0), transposed: [M, N] in the type of x.
+
+    workspace: None allocates what gemm_fp4_groupscale_workspace asks for (nothing up to 32
+    rows); False runs without (K not split); or a device uint8 tensor.
+    """
     f16 = _half(x, "x")
     M, K = x.shape
     N = q.shape[0]
     _need(q, (N, K // 2), torch.uint8, "q")
     e8m0 = _fp4_scale(scale, (N, _groups(K, group)))
     c = _out(c, (M, N), x.dtype, x, "c")
+    if workspace is None and M > 32:
+        workspace = x.new_empty(gemm_fp4_groupscale_workspace(M, N, K), dtype=torch.uint8)
+    ws, wsn = (_ptr(_dev(workspace, torch.uint8, "workspace")), workspace.numel()) if workspace is not None and \
+        workspace is not False and workspace.numel() else (None, 0)
     _check(lib().gemm_fp4_groupscale(_ptr(x), f16, _ld(x, "x"), _ptr(q), _ptr(scale), e8m0, group, M, N, K, _ptr(c),
-                                     _ld(c, "c"), _stream()))
+                                     _ld(c, "c"), ws, wsn, _stream()))
     return c
 
 

@@ -372,6 +372,10 @@ int fp4_quant_groups(const uint16_t* w, int fp16, int64_t ld_w, int64_t rows, in
 int fp4_dequant_groups(const uint8_t* q, const void* scale, int e8m0, int64_t rows, int K, int group,
                        uint16_t* w, int fp16, int64_t ld_w, hipStream_t stream);
 
+/* Host-only workspace query for gemm_fp4_groupscale (no GPU access): the bytes of fp32 partial
+ * sums with which it splits K over more workgroups (0 up to 32 rows). */
+int gemm_fp4_groupscale_workspace(int M, int N, int K, size_t* bytes);
+
 /*
  * Linear layer on 4-bit weights, for few rows (decode):
  *   c[m, n] = round(sum_g scale[n, g] * sum_{k in group g} x[m, k] * e2m1(q[n, k]))
@@ -379,12 +383,15 @@ int fp4_dequant_groups(const uint8_t* q, const void* scale, int e8m0, int64_t ro
  * q      [N, K/2] and scale [N, G] as fp4_quant_groups writes them.
  * c      [M, N] out, the type of x, row stride ldc >= N; fp32 sums, nearest even.
  * Any M and N; the time is the weights' bytes up to about 64 rows, beyond that the weights are
- * read again for every 64 rows.  K % 32 == 0, else MOE355_EUNSUPPORTED.
+ * read again for every 64 rows.  K % 32 == 0 and ld_x up to 2097152, else MOE355_EUNSUPPORTED.
+ * workspace  device memory of gemm_fp4_groupscale_workspace() bytes, 16-byte aligned (contents
+ *            need no initialisation), or NULL: K is then not split (slower from 33 rows on).
+ *            Given but too small: MOE355_EINVAL.
  * The result does not depend on timing: every sum has a fixed order.
  */
 int gemm_fp4_groupscale(const uint16_t* x, int fp16, int64_t ld_x, const uint8_t* q, const void* scale,
                         int e8m0, int group, int M, int N, int K, uint16_t* c, int64_t ldc,
-                        hipStream_t stream);
+                        void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /*
  * Ragged groups: the R rows of x are ordered by expert and expert e owns rows

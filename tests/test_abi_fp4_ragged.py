@@ -34,8 +34,8 @@ def test_fp4_quant_codes(L):
 
 
 def test_gemm_fp4_codes(L):
-    def gemm(x=_p(), fp16=0, ldx=256, q=_p(), s=_p(), e8m0=0, group=64, M=4, N=33, K=256, c=_p(), ldc=33):
-        return L.gemm_fp4_groupscale(x, fp16, ldx, q, s, e8m0, group, M, N, K, c, ldc, None)
+    def gemm(x=_p(), fp16=0, ldx=256, q=_p(), s=_p(), e8m0=0, group=64, M=4, N=33, K=256, c=_p(), ldc=33, ws=None, wsn=0):
+        return L.gemm_fp4_groupscale(x, fp16, ldx, q, s, e8m0, group, M, N, K, c, ldc, ws, wsn, None)
 
     def grouped(x=_p(), fp16=0, ldx=256, q=_p(), s=_p(), e8m0=0, group=64, M=4, N=33, K=256, c=_p(), ldc=33, off=_p(), E=3):
         return L.grouped_gemm_fp4(x, fp16, ldx, q, s, e8m0, group, off, M, E, N, K, c, ldc, None)
@@ -46,6 +46,9 @@ def test_gemm_fp4_codes(L):
         assert f(x=None) == -1 and f(q=None) == -1 and f(s=None) == -1 and f(c=None) == -1
         assert f(x=_p(8)) == -3 and f(q=_p(8)) == -3 and f(ldx=260) == -3 and f(c=_p(1)) == -3
         assert f(M=0, x=None, c=None) == 0 and f(N=0) == 0
+        assert f(ldx=(1 << 21) + 8) == -2
+    # a workspace that is given has to be large enough and aligned
+    assert gemm(M=64, K=8192, ldx=8192, ws=_p(), wsn=64) == -1 and gemm(ws=_p(8)) == -3
     assert grouped(off=None) == -1 and grouped(off=_p(2)) == -3
     assert grouped(E=65536) == -2 and grouped(E=-1) == -1 and grouped(E=0, off=None) == 0
 
@@ -69,3 +72,17 @@ def test_ragged_codes(L):
         assert f(off=_p(2)) == -3
         assert f(E=0, off=None) == 0
     assert fwd(R=0, off=None) == 0 and dgrad(R=0) == 0 and wgrad(N=0) == 0 and wgrad(out=2) == -1
+
+
+def test_gemm_fp4_workspace_query(L):
+    from fp8_block_scaled_grouped_amd import moe355
+    for M in (0, 1, 16, 32):
+        assert moe355.gemm_fp4_groupscale_workspace(M, 18432, 7168) == 0
+    n = moe355.gemm_fp4_groupscale_workspace(64, 2048, 7168)
+    assert n > 0 and n % (64 * 2048 * 4) == 0 and n // (64 * 2048 * 4) <= 7
+    assert moe355.gemm_fp4_groupscale_workspace(64, 2048, 1024) == 0      # one run: nothing to split
+    assert moe355.gemm_fp4_groupscale_workspace(64, 1 << 17, 7168) == 0   # columns enough for every CU
+    for M, N, K, code in ((64, 2048, 48, -2), (-1, 2048, 64, -1)):
+        with pytest.raises(moe355.Moe355Error) as e:
+            moe355.gemm_fp4_groupscale_workspace(M, N, K)
+        assert e.value.code == code
