@@ -46,12 +46,13 @@ __device__ __forceinline__ s16x8 e2m1x8(uint32_t codes, float scale) {
 
 constexpr uint32_t kPastEnd = 0x80000000u;  // a lane offset beyond every descriptor's length
 
-// Buffer descriptor of at most 2^31 - 16 bytes for dma16_buf; lane offsets from `bytes` on read zeros.
+// Buffer descriptor of at most 2^31 - 16 bytes (none for a negative count, which as an unsigned
+// length would check nothing) for dma16_buf; lane offsets from `bytes` on read zeros.
 __device__ __forceinline__ u32x4 dma_buffer(const void* base, int64_t bytes) {
   const uint64_t v = reinterpret_cast<uint64_t>(base);
   return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)v),
                (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(v >> 32)) & 0xffffu,
-               (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)min(bytes, (int64_t)0x7ffffff0)), 0x00020000u};
+               (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)min(max(bytes, (int64_t)0), (int64_t)0x7ffffff0)), 0x00020000u};
 }
 
 // LDS-DMA through a buffer descriptor: lane l moves 16 bytes from base + off to

@@ -16,18 +16,25 @@
 // Zeros on both operands keep a neighbour expert's infinities and NaN out of the sums.
 #include "ragged_gemm.h"
 
+#include <type_traits>
+
 #include "device_common.h"
 #include "frag16.h"
 #include "gemm_engine.h"
 #include "host_common.h"
+#include "skinny.h"
 
 namespace moe355 {
 namespace {
 
 constexpr int kBK = 64;                      // k per step
-// Rotation of the 32-byte column pairs of k-row r in a tile read transposed: the 8 k-rows
-// that half a wave touches in one read land in different banks.
-__device__ __forceinline__ int tr_swz(int r) { return (r & 3) | ((r >> 1) & 4); }
+// Rotation of the 32-byte column pairs of k-row r in a tile of ROWS columns that is read
+// transposed: the 8 k-rows that half a wave touches in one read land in different banks (with 64
+// columns, and so 4 pairs a row, in as many as there are).
+template <int ROWS>
+__device__ __forceinline__ int tr_swz(int r) {
+  return ((r & 3) | ((r >> 1) & 4)) & (ROWS / 16 - 1);
+}
 
 // One operand of the tile: ROWS rows of m (or n); KMAJOR: k runs along memory rows.
 // NW waves fill it with NI DMA instructions each.
@@ -50,17 +57,17 @@ struct Operand {
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         const int r = (w * NI + i) * (64 / CPR) + lane / CPR;
-        const int c = (lane % CPR) ^ (tr_swz(r) << 1);
+        const int c = (lane % CPR) ^ (tr_swz<ROWS>(r) << 1);
         off[i] = 8 * c < cols ? (uint32_t)(r * (ld * 2) + c * 16) : kPastEnd;
       }
     }
   }
-  // krem: k left from this step's first on
-  __device__ __forceinline__ void fetch(u32x4 rsrc, uint32_t lds, int w, int krem) const {
-    const uint32_t past = KMAJOR && kc >= krem ? kPastEnd : 0u;
-#pragma unroll
-    for (int i = 0; i < NI; ++i) dma16_buf(rsrc, off[i] | past, lds + (w * NI + i) * 1024);
+  // DMA i of a step; past: kPastEnd where this lane's k lies past the end
+  __device__ __forceinline__ void dma(int i, u32x4 rsrc, uint32_t lds, int w, uint32_t past) const {
+    dma16_buf(rsrc, off[i] | past, lds + (w * NI + i) * 1024);
   }
+  // krem: k left from this step's first on
+  __device__ __forceinline__ uint32_t past(int krem) const { return KMAJOR && kc >= krem ? kPastEnd : 0u; }
 };
 
 // Fragments of 16 rows x 32 k (lane l: row l % 16, k 8 (l / 16) .. + 7) of a staged operand.
@@ -76,7 +83,7 @@ struct Fragments {
     } else {
       const int r = 8 * g + (i >> 2);
 #pragma unroll
-      for (int f = 0; f < T; ++f) at[f] = r * (2 * ROWS) + ((((row0 >> 4) + f) ^ tr_swz(r)) << 5) + (i & 3) * 8;
+      for (int f = 0; f < T; ++f) at[f] = r * (2 * ROWS) + ((((row0 >> 4) + f) ^ tr_swz<ROWS>(r)) << 5) + (i & 3) * 8;
     }
   }
   __device__ __forceinline__ s16x8 read(uint32_t lds, int f, int half) const {
@@ -213,19 +220,36 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void ragged_gemm_kernel(RaggedArgs
 #pragma unroll
     for (int j = 0; j < TN; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
 
+  // 16-row tiles of this wave that hold rows of the segment: a last, partial tile multiplies no more
+  const int live = min(TM, (mrows - (w / WN) * (BM / WM) + 15) / 16);
   const int steps = (kdim + kBK - 1) / kBK;
+  // DMA i of the next step; steps past the last have descriptors of no length (zeros, no traffic)
+  u32x4 da, db;
+  uint32_t pasta, pastb;
   int fetched = 0;
-  auto fetch = [&](uint32_t stage) {  // DMAs of the next step into a stage; past the last step none
-    if (fetched < steps) {
-      const int krem = kdim - fetched * kBK;
-      oa.fetch(dma_buffer(pa, lena * 2), stage, w, krem);
-      ob.fetch(dma_buffer(pb, lenb * 2), stage + OA::kBytes, w, krem);
-      pa += stepa;
-      pb += stepb;
-      lena -= stepa;
-      lenb -= stepb;
-    }
+  auto next_step = [&] {
+    const int krem = kdim - fetched * kBK;
+    da = dma_buffer(pa, krem > 0 ? lena * 2 : 0);
+    db = dma_buffer(pb, krem > 0 ? lenb * 2 : 0);
+    pasta = oa.past(krem);
+    pastb = ob.past(krem);
+    pa += stepa;
+    pb += stepb;
+    lena -= stepa;
+    lenb -= stepb;
     ++fetched;
+  };
+  auto dma = [&](int i, uint32_t stage) {
+    if (i < OA::NI) {
+      oa.dma(i, da, stage, w, pasta);
+    } else if (i < OA::NI + OB::NI) {
+      ob.dma(i - OA::NI, db, stage + OA::kBytes, w, pastb);
+    }
+  };
+  auto fetch = [&](uint32_t stage) {
+    next_step();
+#pragma unroll
+    for (int i = 0; i < OA::NI + OB::NI; ++i) dma(i, stage);
   };
   s16x8 ra[2][TM], rb[2][TN];
   auto load = [&](uint32_t stage, int half) {
@@ -234,11 +258,34 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void ragged_gemm_kernel(RaggedArgs
 #pragma unroll
     for (int j = 0; j < TN; ++j) rb[half][j] = fb.read(stage + OA::kBytes, j, half);
   };
-  auto multiply = [&](int half) {
+  // The MFMAs of one half step, and between them the fragment reads of the next half (and the DMAs
+  // into the stage that has been read): spread out, they cost the matrix pipe no pause.
+  auto half_step = [&](auto half_c, uint32_t read_stage, auto fill_c, uint32_t fill_stage) {
+    constexpr int kHalf = decltype(half_c)::value, kNext = 1 - kHalf;
+    constexpr bool kFill = decltype(fill_c)::value;
+    constexpr int kDmas = (OA::NI + OB::NI + TM - 1) / TM;
+    constexpr int kReads = (2 * (TM + TN) + TM - 1) / TM;  // a row of MFMAs: all are on their way halfway through
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
+    for (int i = 0; i < TM; ++i) {
+      if constexpr (kFill) {
 #pragma unroll
-      for (int j = 0; j < TN; ++j) acc[i][j] = mfma16x16x32<F16>(rb[half][j], ra[half][i], acc[i][j]);
+        for (int d = 0; d < kDmas; ++d) dma(i * kDmas + d, fill_stage);
+      }
+#pragma unroll
+      for (int d = 0; d < kReads; ++d) {
+        const int f = i * kReads + d;
+        if (f < TN) {
+          rb[kNext][f] = fb.read(read_stage + OA::kBytes, f, kNext);
+        } else if (f < TN + TM) {
+          ra[kNext][f - TN] = fa.read(read_stage, f - TN, kNext);
+        }
+      }
+      if (i < live) {
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] = mfma16x16x32<F16>(rb[kHalf][j], ra[kHalf][i], acc[i][j]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
   };
 
   if (steps > 0) {
@@ -250,15 +297,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void ragged_gemm_kernel(RaggedArgs
     lgkm_wait0();
     uint32_t cur = lds0, other = lds0 + kStage;
     for (int s = 0; s < steps; ++s) {
-      // first half: its fragments are in registers; read the second half's meanwhile
-      load(cur, 1);
-      multiply(0);
+      half_step(std::integral_constant<int, 0>{}, cur, std::false_type{}, 0u);
       lgkm_wait0();
       vm_wait<0>();    // this wave's share of the next step has landed
       barrier_only();  // everyone's has, and nobody reads `cur` any more
-      fetch(cur);
-      load(other, 0);  // of the step after the last: stale values, not used
-      multiply(1);
+      next_step();
+      half_step(std::integral_constant<int, 1>{}, other, std::true_type{}, cur);  // after the last step: stale values, not used
       lgkm_wait0();
       const uint32_t t = cur;
       cur = other;
@@ -307,9 +351,31 @@ int launch(const RaggedArgs& g, hipStream_t stream) {
   return launch_status();
 }
 
+// The tile: 256 x 256 where it makes enough work for the CUs, else 128 x 128, else 64 x 64.  The
+// offsets are on the device, so the number of row tiles is a guess: half a tile more per expert.
+// Measured, us with tiles of 256 / 128 / 64:
+//   fwd   32 experts of 4096 x 2048, 160 rows each on average 167 / 180 / 216, 64 rows 154 / 140 / 145;
+//         2 experts of 2000 x 2000, 500 rows 55 / 29 / 22
+//   dgrad the same 123 / 154 / 192, 110 / 103 / 154; 55 / 28 / 22
+//   wgrad 8 experts of 1536 x 1536, 750 rows 58 / 47 / 58; 64 of 1024 x 1024, 128 rows 59 / 65 / 79
+// The waves stand 4 x 2 in a tile of 256: 8 waves of 128 x 64 (2 x 4) took 3.48 ms where 64 x 128 take
+// 3.39 (32 experts of 4096 x 7168, 65536 rows), 4 waves of 128 x 128 3.52.
+template <int OP, bool OUT32, bool F16>
+int run_type(const RaggedArgs& g, hipStream_t stream) {
+  const int64_t cols = OP == kRaggedFwd ? g.N : g.K, parts = g.E < g.R ? g.E : g.R;
+  auto tiles = [&](int64_t t) {
+    return OP == kRaggedWgrad ? g.E * ceil_div64(g.N, t) * ceil_div64(g.K, t)
+                              : (g.R / t + (parts + 1) / 2) * ceil_div64(cols, t);
+  };
+  if (OP == kRaggedWgrad ? tiles(256) >= 512 : tiles(256) >= 200 && g.R >= 112ll * g.E)
+    return launch<OP, F16, OUT32, 256, 256, 4, 2>(g, stream);
+  if (tiles(128) >= 192) return launch<OP, F16, OUT32, 128, 128, 4, 2>(g, stream);
+  return launch<OP, F16, OUT32, 64, 64, 2, 2>(g, stream);
+}
+
 template <int OP, bool OUT32 = false>
 int run(const RaggedArgs& g, int f16, hipStream_t stream) {
-  return f16 ? launch<OP, true, OUT32, 256, 256, 2, 4>(g, stream) : launch<OP, false, OUT32, 256, 256, 2, 4>(g, stream);
+  return f16 ? run_type<OP, OUT32, true>(g, stream) : run_type<OP, OUT32, false>(g, stream);
 }
 
 bool aligned_rows(const void* p, int64_t ld) { return aligned16(p) && ld % 8 == 0; }
@@ -337,6 +403,12 @@ extern "C" int grouped_gemm(const uint16_t* x, int fp16, int64_t ld_x, const uin
   if (R == 0 || E == 0 || N == 0) return MOE355_OK;
   MOE355_CHECK(offsets && y && (K == 0 || (x && w)), MOE355_EINVAL);
   MOE355_CHECK((K == 0 || (aligned_rows(x, ld_x) && aligned16(w))) && aligned_rows(y, ld_y) && aligned4(offsets), MOE355_EMISALIGNED);
+  // few rows an expert: the weights' bytes bound it (32 experts of 4096 x 2048, 4 rows each: 97 us against
+  // 124 with the best tile; 32 rows 133 both, and an expert with more rows than most costs less there)
+  if (R <= 8ll * E && K > 0)
+    return launch_skinny(SkinnyArgs{x, reinterpret_cast<const uint8_t*>(w), nullptr, offsets, y, ld_x, ld_y, R, E, N, K,
+                                    1, nullptr},
+                         kW16, 128, fp16, stream);
   return run<kRaggedFwd>(RaggedArgs{x, w, y, offsets, ld_x, K, ld_y, R, E, N, K}, fp16, stream);
 }
 

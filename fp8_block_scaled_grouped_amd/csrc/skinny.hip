@@ -377,7 +377,11 @@ __global__ __launch_bounds__(256) void skinny_reduce_kernel(SkinnyArgs a) {
 template <int W, int GROUP, bool F16, int MR, int CT, int CW, int KW, int H, int S, int NP>
 int launch_tile(SkinnyArgs g, hipStream_t stream) {
   using Sk = Skinny<W, GROUP, F16, MR, CT, CW, KW, H, S, NP>;
-  const int64_t nx = ceil_div64(g.N, Sk::NC), nz = (g.offsets ? 1 : ceil_div64(g.R, MR)) * g.splits;
+  const int64_t nx = ceil_div64(g.N, Sk::NC), passes = ceil_div64(g.R, MR);
+  // Passes of one expert run side by side while the grid is small (an expert may hold most of the rows);
+  // a large grid of mostly empty workgroups would cost more than it gives.
+  const int64_t side = 4096 / (nx * g.E) > 1 ? 4096 / (nx * g.E) : 1;
+  const int64_t nz = (g.offsets ? (passes < side ? passes : side) : passes) * g.splits;
   MOE355_CHECK(nx < (1ll << 31) && nz < 65536, MOE355_EUNSUPPORTED);
   auto* fn = &skinny_kernel<W, GROUP, F16, MR, CT, CW, KW, H, S, NP>;
   const int lds = Sk::lds_bytes(g.K), G = (g.K + GROUP - 1) / GROUP;

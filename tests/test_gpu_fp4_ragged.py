@@ -148,6 +148,36 @@ def test_gemm_fp4_wide(m, M):
         _close(c, xf @ w.T, np.abs(xf) @ np.abs(w).T, K, "bf16", "gemm %dx%dx%d" % (M, N, K))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("group,fmt", [(32, "fp32"), (32, "e8m0"), (64, "e8m0"), (128, "fp32")])
+@pytest.mark.parametrize("N,K,rows", [(40, 4160, (2, 9, 20, 40, 64)), (7000, 4160, (2, 9, 40)), (33000, 160, (2, 9, 20, 64))])
+def test_gemm_fp4_tilings(m, dtype, group, fmt, N, K, rows):
+    # few, some and many columns with every row tile: each tiling of the kernel, several windows of scales
+    # and scale rows that do not start on whole dwords
+    q, s, w = _packed((N, K), group, fmt, N)
+    for M in rows:
+        print("fp4 tiling", dtype, group, fmt, N, K, M, flush=True)
+        x = _randn((M, K), dtype, M)
+        xf = _f64(x)
+        ref, mag = xf @ w.T, np.abs(xf) @ np.abs(w).T
+        _close(m.gemm_fp4_groupscale(x.to(DEV), q, s, group), ref, mag, K, dtype, "M %d" % M)
+        if M > 32:
+            _close(m.gemm_fp4_groupscale(x.to(DEV), q, s, group, workspace=False), ref, mag, K, dtype, "no workspace")
+
+
+def test_gemm_fp4_workspace(m):
+    x, (q, s, _) = _randn((64, 8192), "bf16", 1).to(DEV), _packed((520, 8192), 64, "fp32", 2)
+    n = m.gemm_fp4_groupscale_workspace(64, 520, 8192)
+    assert n > 0
+    want = m.gemm_fp4_groupscale(x, q, s, 64)
+    for fill in (0, 255):   # its contents do not matter, and nothing is written past it
+        ws = torch.full((n + 256,), fill, dtype=torch.uint8, device=DEV)
+        assert torch.equal(m.gemm_fp4_groupscale(x, q, s, 64, workspace=ws[:n]), want)
+        assert bool((ws[n:] == fill).all())
+    with pytest.raises(m.Moe355Error):
+        m.gemm_fp4_groupscale(x, q, s, 64, workspace=ws[:n - 16])
+
+
 def test_gemm_fp4_strided_and_odd_columns(m):
     for N in (1, 7, 63):
         x, (q, s, w) = _randn((5, 128), "bf16", 1), _packed((N, 128), 64, "fp32", 2)
@@ -229,6 +259,37 @@ def test_grouped_gemm_and_gradients(m, dtype, counts, N, K):
         for e in range(E):
             if counts[e] == 0:
                 assert bool((dw[e] == 0).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("op,N,K", [("fwd", 5128, 136), ("fwd", 5120, 64), ("dgrad", 136, 5128), ("dgrad", 200, 5120),
+                                    ("wgrad", 2600, 2568), ("wgrad", 1288, 1304)])
+def test_ragged_largest_tiles(m, op, dtype, N, K):
+    # enough work for the largest tile, with segments that end anywhere in one; inner sizes off its step
+    counts = [700, 0, 1300, 513, 1] if op != "wgrad" else [200, 0, 97, 64, 1] * (1 if N > 2000 else 4)
+    print("ragged large", op, dtype, N, K, flush=True)
+    off, R, E = _offsets(counts), sum(counts), len(counts)
+    x, w, dy = _randn((R, K), dtype, R), _randn((E, N, K), dtype, N, 0.05), _randn((R, N), dtype, K, 0.1)
+    od = _dev_offsets(off)
+    if op == "fwd":
+        got, (ref, mag), n = m.grouped_gemm(x.to(DEV), w.to(DEV), od), ragged.forward(_f64(x), _f64(w), off), K
+    elif op == "dgrad":
+        got, (ref, mag), n = m.grouped_gemm_dgrad(dy.to(DEV), w.to(DEV), od), ragged.dgrad(_f64(dy), _f64(w), off), N
+    else:
+        got, (ref, mag), n = m.grouped_gemm_wgrad(dy.to(DEV), x.to(DEV), od), ragged.wgrad(_f64(dy), _f64(x), off), max(counts)
+    _close(got, ref, mag, n, dtype, op)
+
+
+def test_one_expert_with_most_rows(m):
+    # few rows an expert on average, nearly all of them in one: its passes
+    counts, N, K = [0] * 9 + [150] + [1] * 30, 264, 320
+    off, R = _offsets(counts), sum(counts)
+    x, w = _randn((R, K), "bf16", 1), _randn((40, N, K), "bf16", 2, 0.05)
+    ref, mag = ragged.forward(_f64(x), _f64(w), off)
+    _close(m.grouped_gemm(x.to(DEV), w.to(DEV), _dev_offsets(off)), ref, mag, K, "bf16", "16-bit weights")
+    q, s, wf = _packed((40, N, K), 32, "e8m0", 3)
+    ref, mag = ragged.forward(_f64(x), wf, off)
+    _close(m.grouped_gemm_fp4(x.to(DEV), q, s, _dev_offsets(off), 32), ref, mag, K, "bf16", "4-bit weights")
 
 
 def test_ragged_strided_rows(m):
