@@ -524,3 +524,65 @@ def test_binding_refuses(m):
         with pytest.raises(m.Moe355Error) as err:
             f()
         assert err.value.code == code
+
+
+# ------------------------------------------------------------------ together
+def _layer64(x, ids, weights, w1, w2, s1, s2):
+    """The example's layer in 64 bits, and a bound of what bf16 between the products costs: with u = 2^-8,
+    gate, up and h are each rounded once (SiLU's relative slope stays below 1.3 + |gate|, taken as it
+    is), y and the shared product once more."""
+    silu = lambda v: v / (1 + np.exp(-v))  # noqa: E731
+    u = 2.0 ** -8
+
+    def gated(rows, a, b):
+        z, zm = rows @ a.T, np.abs(rows) @ np.abs(a).T
+        i = a.shape[0] // 2
+        gate, up = z[:, :i], z[:, i:]
+        h = silu(gate) * up
+        dg, du = u * np.abs(gate) + 1e-5 * zm[:, :i], u * np.abs(up) + 1e-5 * zm[:, i:]
+        dh = 1.1 * dg * (np.abs(up) + du) + np.abs(silu(gate)) * du    # |SiLU'| < 1.1
+        dh = dh + u * (np.abs(h) + dh)
+        y, ym = h @ b.T, np.abs(h) @ np.abs(b).T
+        dy = dh @ np.abs(b).T + 1e-5 * ym
+        return y, dy + u * (np.abs(y) + dy)
+
+    out, tol = gated(x, s1, s2)
+    for t in range(x.shape[0]):
+        for j, e in enumerate(ids[t]):
+            y, d = gated(x[t:t + 1], w1[e], w2[e])
+            out[t] += weights[t, j] * y[0]
+            tol[t] += abs(weights[t, j]) * d[0] * 1.001
+    return out, tol + 1e-5 * np.abs(out) + 1e-6
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("T", [1, 40])
+def test_example_layer(m, packed, T):
+    from fp8_block_scaled_grouped_amd.examples.ragged_experts import RaggedExperts
+    layer = RaggedExperts(H=64, I=96, E=8, n_group=4, topk_group=2, topk=3, device=DEV, seed=3)
+    x, logits = _randn((T, 64), "bf16", T).to(DEV), torch.randn((T, 8), generator=torch.Generator().manual_seed(T)).to(DEV)
+    names = ("w1", "w2", "s1", "s2")
+    if packed:
+        layer.pack(32, "e8m0")
+        ws = [fp4.dequant_groups(q.cpu().numpy(), s.cpu().numpy(), 32) for q, s in (layer.packed[n] for n in names)]
+    else:
+        ws = [_f64(getattr(layer, n).to(torch.bfloat16)) for n in names]
+    weights, ids = m.grouped_topk(logits, layer.bias, *layer.route)
+    ref, tol = _layer64(_f64(x), ids.cpu().numpy(), _f64(weights), *ws)
+    err = np.abs(_f64(layer(x, logits)) - ref)
+    assert (err <= tol).all(), float((err / tol).max())
+
+
+def test_example_trains_and_packs(m):
+    from fp8_block_scaled_grouped_amd.examples.ragged_experts import RaggedExperts, train
+    shape = dict(H=128, I=64, E=8, n_group=4, topk_group=2, topk=2, device=DEV)
+    layer, teacher = RaggedExperts(**shape, seed=1), RaggedExperts(**shape, seed=2)
+    x = _randn((256, 128), "bf16", 1).to(DEV)
+    logits = torch.randn((256, 8), generator=torch.Generator().manual_seed(2)).to(DEV)
+    losses = train(layer, teacher, x, logits, 15).cpu()
+    assert bool(torch.isfinite(losses).all()) and float(losses[-1]) < 0.9 * float(losses[0])
+    assert all(p.grad is not None and bool(torch.isfinite(p.grad).all()) for p in layer.parameters())
+    before = layer(x, logits).detach()
+    after = layer.pack()(x, logits)
+    # 4-bit weights: each product's weights are off by at most half a step of e2m1, 1/6 of their value at worst
+    assert float((after - before).norm() / before.norm()) < 0.5
