@@ -162,7 +162,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void ragged_gemm_kernel(RaggedArgs
   using OA = Operand<BM, NW, AK>;
   using OB = Operand<BN, NW, BK>;
   constexpr int kStage = OA::kBytes + OB::kBytes;
-  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ __align__(16) uint8_t smem[2 * kStage];
   const int tid = threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
 
@@ -337,17 +337,13 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void ragged_gemm_kernel(RaggedArgs
 template <int OP, bool F16, bool OUT32, int BM, int BN, int WM, int WN>
 int launch(const RaggedArgs& g, hipStream_t stream) {
   auto* fn = &ragged_gemm_kernel<OP, F16, OUT32, BM, BN, WM, WN>;
-  constexpr int kLds = 2 * (BM + BN) * kBK * 2;
   const int64_t nt = ceil_div64(OP == kRaggedFwd ? g.N : g.K, BN);
   // an upper bound of the row tiles: the offsets are on the device
   const int64_t mt = OP == kRaggedWgrad ? (int64_t)g.E * ceil_div64(g.N, BM)
                                         : g.R / BM + (g.E < g.R ? g.E : g.R);
   const int64_t grid = ceil_div64(mt * nt, 8) * 8;
   MOE355_CHECK(grid < (1ll << 31), MOE355_EUNSUPPORTED);
-  if (hipFuncSetAttribute(reinterpret_cast<const void*>(fn), hipFuncAttributeMaxDynamicSharedMemorySize, kLds) !=
-      hipSuccess)
-    return MOE355_ELAUNCH;
-  hipLaunchKernelGGL(fn, dim3((unsigned)grid), dim3(64 * WM * WN), kLds, stream, g);
+  hipLaunchKernelGGL(fn, dim3((unsigned)grid), dim3(64 * WM * WN), 0, stream, g);
   return launch_status();
 }
 

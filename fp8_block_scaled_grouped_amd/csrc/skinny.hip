@@ -139,6 +139,7 @@ struct Skinny {
   static constexpr int kSpan = kWindowStages * kK;                     // and its k
   static constexpr int kWindow = kSpan / GROUP;                        // and its scales of a row
   static_assert(kWindowStages >= S, "a window of scales outlives the stages in flight");
+  static_assert(S * kStage + (W == kW16 ? 0 : 2 * NC * kWindow * Fm::kScaleBytes) <= 160 * 1024, "LDS of a workgroup");
   static_assert(kDmaW % NP == 0 && kDmaX % NP == 0, "the copying waves share the DMAs evenly");
   static_assert(kWBytes % 1024 == 0 && kXBytes % 1024 == 0, "whole DMAs");
   static int stages(int K) { return (K + kK - 1) / kK; }
@@ -386,9 +387,6 @@ int launch_tile(SkinnyArgs g, hipStream_t stream) {
   auto* fn = &skinny_kernel<W, GROUP, F16, MR, CT, CW, KW, H, S, NP>;
   const int lds = Sk::lds_bytes(g.K), G = (g.K + GROUP - 1) / GROUP;
   const int loose = W == kFp4E8M0 && (G % 4 != 0 || (reinterpret_cast<uintptr_t>(g.scale) & 3u) != 0);
-  if (hipFuncSetAttribute(reinterpret_cast<const void*>(fn), hipFuncAttributeMaxDynamicSharedMemorySize, lds) !=
-      hipSuccess)
-    return MOE355_ELAUNCH;
   hipLaunchKernelGGL(fn, dim3((unsigned)nx, (unsigned)g.E, (unsigned)nz), dim3((CW * KW + NP) * 64), lds, stream, g,
                      Sk::scale_slots(g.K), loose);
   if (g.splits > 1)
@@ -397,35 +395,65 @@ int launch_tile(SkinnyArgs g, hipStream_t stream) {
   return launch_status();
 }
 
+// One matrix, more than 16 rows: 128 columns a workgroup where that gives half of the CUs one.
+bool skinny_wide(int64_t M, int64_t N) { return ceil_div64(N, 128) * ceil_div64(M, M <= 32 ? 32 : 64) >= 128; }
+
+// The tiling of a launch.  Rows of a pass (MR): the rows of a matrix, of an expert on average; one that
+// has more takes another pass over weights that the caches still hold.  Columns of a workgroup: as many
+// as still give the CUs enough workgroups.  Measured, us (4-bit weights; the choice first):
+//   1 row, 2048 x 7168:      16 columns 6.4, 32 columns 9.2
+//   1 row, 18432 x 7168:     32 columns 15.7, 16 16.3, 64 17.2
+//   8 rows, 4096 x 7168:     8 rows a pass 7.8, 16 8.4
+//   16 rows, 18432 x 7168:   32 columns 19.9 (one block a stage; two 20.6), 128 columns 21.5
+//   32 rows, 18432 x 7168:   128 columns with K in two 21.8, K in one 25.1
+//   64 rows, 18432 x 7168:   128 columns with K in two 35.4, 256 columns and 3 runs of K 36.5
+//   64 rows, 2048 x 7168:    64 columns and 7 runs of K 13.3, 1 run 25.2
+//   one token's 8 experts of 4096 x 7168: 64 columns 34.0, 128 38.1
+//   64 tokens, top-8 of 256 experts of 7168 x 2048: 128 columns 283, 64 324; of 4096 x 7168: 577, 575
+//   2048 rows over 64 experts of 4096 x 7168: 64 rows a pass 297, 32 388
 template <int W, int GROUP, bool F16>
 int launch(const SkinnyArgs& g, hipStream_t stream) {
   constexpr int H = W == kW16 ? 1 : 2;  // 4-bit rows: whole 128-byte lines
-  constexpr int MR = W == kW16 ? 8 : 4;
-  const int rows = g.offsets ? (int)ceil_div64(g.R, g.E) : g.R;  // of a matrix, on average
   const int64_t mats = g.offsets && g.R < g.E ? g.R : g.E;       // with rows, at most
-  // Columns of a workgroup: 64 where that still makes two workgroups for every CU (then their K
-  // is walked by one wave: no tiles to add; 256 experts of 4096 x 7168, 512 rows: 591 us against 616
-  // with 32 columns), 16 where 32 would leave a quarter of the CUs idle (2048 x 7168, 1 row: 6.8
-  // against 9.4 us), else 32 (18432 x 7168, 1 row: 15.5 against 18.3 with 16 and 20.2 with 64).
-  const bool wide = ceil_div64(g.N, 64) * mats >= 512, narrow = ceil_div64(g.N, 32) * mats < 192;
-  // Rows of a pass: of an expert on average some have more, and then take another pass over
-  // weights that the caches still hold (512 rows over 256 experts of 7168 x 2048: 302 us with 4
-  // rows a pass, 366 with 16, whose empty rows cost DMAs).
-  if (rows <= (g.offsets ? 2 : 4)) {
-    if (wide) return launch_tile<W, GROUP, F16, MR, 1, 4, 1, H, 4, 2>(g, stream);
-    if (narrow) return launch_tile<W, GROUP, F16, MR, 1, 1, 4, H, 3, 2>(g, stream);
-    return launch_tile<W, GROUP, F16, MR, 1, 2, 2, H, 3, 2>(g, stream);
+  const int64_t rows = g.offsets ? ceil_div64(g.R, g.E) : g.R;  // of a matrix, on average
+  auto groups = [&](int cols) { return ceil_div64(g.N, cols) * mats; };
+  if constexpr (W != kW16) {
+    if (!g.offsets && rows <= 4) {
+      if (groups(64) >= 512) return launch_tile<W, GROUP, F16, 4, 2, 2, 2, H, 3, 2>(g, stream);
+      if (groups(32) < 192) return launch_tile<W, GROUP, F16, 4, 1, 1, 4, H, 3, 4>(g, stream);
+      return launch_tile<W, GROUP, F16, 4, 1, 2, 2, H, 3, 2>(g, stream);
+    }
+  }
+  if (rows <= (g.offsets ? 4 : 8)) {
+    if (groups(128) >= 1024) return launch_tile<W, GROUP, F16, 8, 2, 4, 1, H, 3, W == kW16 ? 2 : 4>(g, stream);
+    if (groups(64) >= 512) return launch_tile<W, GROUP, F16, 8, 2, 2, 2, H, W == kW16 ? 4 : 3, 2>(g, stream);
+    if (groups(32) < 192) return launch_tile<W, GROUP, F16, 8, 1, 1, 4, H, 3, 4>(g, stream);
+    return launch_tile<W, GROUP, F16, 8, 1, 2, 2, H, 3, 2>(g, stream);
   }
   if (rows <= (g.offsets ? 12 : 16)) {
-    if (wide) return launch_tile<W, GROUP, F16, 16, 1, 4, 1, H, 4, 2>(g, stream);
-    if (narrow) return launch_tile<W, GROUP, F16, 16, 1, 1, 4, H, 3, 2>(g, stream);
-    return launch_tile<W, GROUP, F16, 16, 1, 2, 2, H, 3, 2>(g, stream);
+    if (groups(128) >= 1024) return launch_tile<W, GROUP, F16, 16, 2, 4, 1, H, 3, 4>(g, stream);
+    if (groups(64) >= 512) return launch_tile<W, GROUP, F16, 16, 2, 2, 2, 1, 3, 4>(g, stream);
+    if (groups(32) < 192) return launch_tile<W, GROUP, F16, 16, 1, 1, 4, H, 3, 4>(g, stream);
+    return launch_tile<W, GROUP, F16, 16, 1, 2, 2, 1, 4, 2>(g, stream);
   }
-  if (rows <= 32) return launch_tile<W, GROUP, F16, 32, 2, 4, 1, H, 3, 2>(g, stream);
-  if constexpr (W == kW16 || (W == kFp4 && GROUP == 32)) {  // 256 columns' weights or scales do not fit
-    return launch_tile<W, GROUP, F16, 64, 2, 4, 1, 1, 3, 4>(g, stream);
-  } else {
-    return launch_tile<W, GROUP, F16, 64, 4, 4, 1, 1, 3, 4>(g, stream);
+  if constexpr (W == kW16) return MOE355_EUNSUPPORTED;  // more rows are the tiled product's
+  if constexpr (W != kW16) {
+    if (g.offsets) {
+      if (rows <= 20) return launch_tile<W, GROUP, F16, 32, 2, 4, 1, 1, 4, 4>(g, stream);
+      if constexpr (W == kFp4 && GROUP == 32) {  // 256 columns' scales do not fit
+        return launch_tile<W, GROUP, F16, 64, 2, 4, 1, 1, 3, 4>(g, stream);
+      } else {
+        return launch_tile<W, GROUP, F16, 64, 4, 4, 1, 1, 3, 4>(g, stream);
+      }
+    }
+    const bool wide = skinny_wide(g.R, g.N);
+    if (rows <= 32) {
+      if (wide) return launch_tile<W, GROUP, F16, 32, 2, 4, 2, 1, 3, 8>(g, stream);
+      return launch_tile<W, GROUP, F16, 32, 1, 4, 2, 1, 3, 4>(g, stream);
+    }
+    constexpr int S = W == kFp4 && GROUP < 128 ? 2 : 3;  // three stages and the fp32 scales do not fit
+    if (wide) return launch_tile<W, GROUP, F16, 64, 2, 4, 2, 1, S, 4>(g, stream);
+    return launch_tile<W, GROUP, F16, 64, 1, 4, 2, 1, 3, 4>(g, stream);
   }
 }
 
@@ -441,10 +469,9 @@ int by_group(const SkinnyArgs& g, int group, hipStream_t stream) {
 }  // namespace
 
 int skinny_splits(int M, int N, int K) {
-  if (M <= 32) return 1;
-  // 256 columns and 64 rows a workgroup, one workgroup a CU: as many runs of K as fill the 256
-  // CUs, of at least 8 stages of 128
-  const int64_t tiles = ceil_div64(N, 256) * ceil_div64(M, 64), runs = ceil_div64(K, 1024);
+  if (M <= 16 || skinny_wide(M, N)) return 1;
+  // 64 columns a workgroup: as many runs of K, of at least 1024, as give each of the 256 CUs one
+  const int64_t tiles = ceil_div64(N, 64) * ceil_div64(M, M <= 32 ? 32 : 64), runs = ceil_div64(K, 1024);
   const int64_t s = tiles >= 256 ? 1 : 256 / tiles;
   return (int)(s < runs ? s : runs);
 }

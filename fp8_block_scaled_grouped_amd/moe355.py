@@ -543,7 +543,7 @@ def gemm_fp4_groupscale(x, q, scale, group=128, c=None, workspace=None):
     """x bf16 or fp16 [M, K] times 4-bit weights q [N, K/2] with scales [N, ceil(K/group)] (fp32, or
     uint8 for E8M0), transposed: [M, N] in the type of x.
 
-    workspace: None allocates what gemm_fp4_groupscale_workspace asks for (nothing up to 32
+    workspace: None allocates what gemm_fp4_groupscale_workspace asks for (nothing up to 16
     rows); False runs without (K not split); or a device uint8 tensor.
     """
     f16 = _half(x, "x")
@@ -552,7 +552,7 @@ def gemm_fp4_groupscale(x, q, scale, group=128, c=None, workspace=None):
     _need(q, (N, K // 2), torch.uint8, "q")
     e8m0 = _fp4_scale(scale, (N, _groups(K, group)))
     c = _out(c, (M, N), x.dtype, x, "c")
-    if workspace is None and M > 32:
+    if workspace is None and M > 16:
         workspace = x.new_empty(gemm_fp4_groupscale_workspace(M, N, K), dtype=torch.uint8)
     ws, wsn = (_ptr(_dev(workspace, torch.uint8, "workspace")), workspace.numel()) if workspace is not None and \
         workspace is not False and workspace.numel() else (None, 0)

@@ -373,7 +373,8 @@ int fp4_dequant_groups(const uint8_t* q, const void* scale, int e8m0, int64_t ro
                        uint16_t* w, int fp16, int64_t ld_w, hipStream_t stream);
 
 /* Host-only workspace query for gemm_fp4_groupscale (no GPU access): the bytes of fp32 partial
- * sums with which it splits K over more workgroups (0 up to 32 rows). */
+ * sums with which it splits K over more workgroups (0 up to 16 rows, and where
+ * the columns alone give the GPU enough work). */
 int gemm_fp4_groupscale_workspace(int M, int N, int K, size_t* bytes);
 
 /*
@@ -385,7 +386,7 @@ int gemm_fp4_groupscale_workspace(int M, int N, int K, size_t* bytes);
  * Any M and N; the time is the weights' bytes up to about 64 rows, beyond that the weights are
  * read again for every 64 rows.  K % 32 == 0 and ld_x up to 2097152, else MOE355_EUNSUPPORTED.
  * workspace  device memory of gemm_fp4_groupscale_workspace() bytes, 16-byte aligned (contents
- *            need no initialisation), or NULL: K is then not split (slower from 33 rows on).
+ *            need no initialisation), or NULL: K is then not split (slower from 17 rows on).
  *            Given but too small: MOE355_EINVAL.
  * The result does not depend on timing: every sum has a fixed order.
  */

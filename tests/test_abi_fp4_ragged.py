@@ -76,8 +76,8 @@ def test_ragged_codes(L):
 
 def test_gemm_fp4_workspace_query(L):
     from fp8_block_scaled_grouped_amd import moe355
-    for M in (0, 1, 16, 32):
-        assert moe355.gemm_fp4_groupscale_workspace(M, 18432, 7168) == 0
+    for M in (0, 1, 16):
+        assert moe355.gemm_fp4_groupscale_workspace(M, 2048, 7168) == 0
     n = moe355.gemm_fp4_groupscale_workspace(64, 2048, 7168)
     assert n > 0 and n % (64 * 2048 * 4) == 0 and n // (64 * 2048 * 4) <= 7
     assert moe355.gemm_fp4_groupscale_workspace(64, 2048, 1024) == 0      # one run: nothing to split
