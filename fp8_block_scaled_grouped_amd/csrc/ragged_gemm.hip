@@ -342,7 +342,7 @@ int launch(const RaggedArgs& g, hipStream_t stream) {
   const int64_t mt = OP == kRaggedWgrad ? (int64_t)g.E * ceil_div64(g.N, BM)
                                         : g.R / BM + (g.E < g.R ? g.E : g.R);
   const int64_t grid = ceil_div64(mt * nt, 8) * 8;
-  MOE355_CHECK(grid < (1ll << 31), MOE355_EUNSUPPORTED);
+  MOE355_CHECK(grid * (64 * WM * WN) < (1ll << 32), MOE355_EUNSUPPORTED);  // threads of a launch
   hipLaunchKernelGGL(fn, dim3((unsigned)grid), dim3(64 * WM * WN), 0, stream, g);
   return launch_status();
 }

@@ -629,6 +629,7 @@ class _GroupedLinear(torch.autograd.Function):
         return grouped_gemm(x, w, offsets)
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         x, w, offsets = ctx.saved_tensors
         dy = dy.contiguous()
