@@ -455,17 +455,16 @@ _F16 = {torch.bfloat16: 0, torch.float16: 1}
 
 def _half(t, name):
     """0 for a bf16 device tensor, 1 for an fp16 one."""
-    if not t.is_cuda:
-        raise ValueError("%s must be a GPU tensor" % name)
-    if t.dtype not in _F16:
-        raise ValueError("%s must be bf16 or fp16, got %s" % (name, t.dtype))
-    return _F16[t.dtype]
+    f16 = _F16.get(t.dtype)
+    if f16 is None or not t.is_cuda:
+        raise ValueError("%s must be a bf16 or fp16 GPU tensor, got %s on %s" % (name, t.dtype, t.device))
+    return f16
 
 
 def _out(t, shape, dtype, like, name):
     """The output tensor: allocated when None, else checked (2-D outputs may have strided rows)."""
     if t is None:
-        return like.new_empty(shape, dtype=dtype)
+        return like.new_empty(shape) if like.dtype == dtype else like.new_empty(shape, dtype=dtype)
     _dev(t, dtype, name)
     if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
