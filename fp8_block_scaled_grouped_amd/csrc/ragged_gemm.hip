@@ -161,8 +161,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void ragged_gemm_kernel(RaggedArgs
   constexpr int NW = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
   using OA = Operand<BM, NW, AK>;
   using OB = Operand<BN, NW, BK>;
-  constexpr int kStage = OA::kBytes + OB::kBytes;
-  __shared__ __align__(16) uint8_t smem[2 * kStage];
+  constexpr int kSlot = OA::kBytes > OB::kBytes ? OA::kBytes : OB::kBytes;
+  __shared__ __align__(16) uint8_t smem[5 * kSlot];
   const int tid = threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
 
@@ -223,61 +223,63 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void ragged_gemm_kernel(RaggedArgs
   // 16-row tiles of this wave that hold rows of the segment: a last, partial tile multiplies no more
   const int live = min(TM, (mrows - (w / WN) * (BM / WM) + 15) / 16);
   const int steps = (kdim + kBK - 1) / kBK;
-  // DMA i of the next step; steps past the last have descriptors of no length (zeros, no traffic)
+  // The operands of the steps, A(0) B(0) A(1) B(1) .., take the slots of a ring of five in turn.  Past the
+  // last step the descriptors have no length (zeros, no traffic).
   u32x4 da, db;
   uint32_t pasta, pastb;
-  int fetched = 0;
-  auto next_step = [&] {
-    const int krem = kdim - fetched * kBK;
-    da = dma_buffer(pa, krem > 0 ? lena * 2 : 0);
-    db = dma_buffer(pb, krem > 0 ? lenb * 2 : 0);
-    pasta = oa.past(krem);
-    pastb = ob.past(krem);
+  int ka = 0, kb = 0;  // first k of the next A and B
+  auto next_a = [&] {
+    da = dma_buffer(pa, ka < kdim ? lena * 2 : 0);
+    pasta = oa.past(kdim - ka);
     pa += stepa;
-    pb += stepb;
     lena -= stepa;
+    ka += kBK;
+  };
+  auto next_b = [&] {
+    db = dma_buffer(pb, kb < kdim ? lenb * 2 : 0);
+    pastb = ob.past(kdim - kb);
+    pb += stepb;
     lenb -= stepb;
-    ++fetched;
+    kb += kBK;
   };
-  auto dma = [&](int i, uint32_t stage) {
-    if (i < OA::NI) {
-      oa.dma(i, da, stage, w, pasta);
-    } else if (i < OA::NI + OB::NI) {
-      ob.dma(i - OA::NI, db, stage + OA::kBytes, w, pastb);
-    }
-  };
-  auto fetch = [&](uint32_t stage) {
-    next_step();
+  auto fetch = [&](uint32_t slot_a, uint32_t slot_b) {
+    next_a();
 #pragma unroll
-    for (int i = 0; i < OA::NI + OB::NI; ++i) dma(i, stage);
+    for (int i = 0; i < OA::NI; ++i) oa.dma(i, da, slot_a, w, pasta);
+    next_b();
+#pragma unroll
+    for (int i = 0; i < OB::NI; ++i) ob.dma(i, db, slot_b, w, pastb);
   };
   s16x8 ra[2][TM], rb[2][TN];
-  auto load = [&](uint32_t stage, int half) {
-#pragma unroll
-    for (int i = 0; i < TM; ++i) ra[half][i] = fa.read(stage, i, half);
-#pragma unroll
-    for (int j = 0; j < TN; ++j) rb[half][j] = fb.read(stage + OA::kBytes, j, half);
-  };
-  // The MFMAs of one half step, and between them the fragment reads of the next half (and the DMAs
-  // into the stage that has been read): spread out, they cost the matrix pipe no pause.
-  auto half_step = [&](auto half_c, uint32_t read_stage, auto fill_c, uint32_t fill_stage) {
+  // The MFMAs of half a step, and spread between them the fragment reads of the next half and the DMAs of
+  // one operand (the first half A's, the second B's).  DMAs in a burst cost: with all 8 at the start of
+  // one half the product of 65536 rows over 32 experts of 4096 x 7168 took 3.76 ms, spread over that
+  // half 3.46, over both 3.32.
+  auto half_step = [&](auto half_c, uint32_t read_a, uint32_t read_b, uint32_t fill) {
     constexpr int kHalf = decltype(half_c)::value, kNext = 1 - kHalf;
-    constexpr bool kFill = decltype(fill_c)::value;
-    constexpr int kDmas = (OA::NI + OB::NI + TM - 1) / TM;
-    constexpr int kReads = (2 * (TM + TN) + TM - 1) / TM;  // a row of MFMAs: all are on their way halfway through
+    constexpr int kCount = kHalf == 0 ? OA::NI : OB::NI, kDmas = (kCount + TM - 1) / TM;
+    // reads a row of MFMAs: all are on their way after half of the rows (transposed ones, of two
+    // instructions each, after three quarters: dgrad 3.36 ms against 3.43, wgrad 3.35 against 3.44, while fwd
+    // went from 3.22 to 3.29)
+    constexpr int kReads = OP == kRaggedFwd ? (2 * (TM + TN) + TM - 1) / TM : (4 * (TM + TN) + 3 * TM - 1) / (3 * TM);
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
-      if constexpr (kFill) {
 #pragma unroll
-        for (int d = 0; d < kDmas; ++d) dma(i * kDmas + d, fill_stage);
+      for (int d = 0; d < kDmas; ++d) {
+        if (i * kDmas + d >= kCount) break;
+        if constexpr (kHalf == 0) {
+          oa.dma(i * kDmas + d, da, fill, w, pasta);
+        } else {
+          ob.dma(i * kDmas + d, db, fill, w, pastb);
+        }
       }
 #pragma unroll
       for (int d = 0; d < kReads; ++d) {
         const int f = i * kReads + d;
         if (f < TN) {
-          rb[kNext][f] = fb.read(read_stage + OA::kBytes, f, kNext);
+          rb[kNext][f] = fb.read(read_b, f, kNext);
         } else if (f < TN + TM) {
-          ra[kNext][f - TN] = fa.read(read_stage, f - TN, kNext);
+          ra[kNext][f - TN] = fa.read(read_a, f - TN, kNext);
         }
       }
       if (i < live) {
@@ -289,24 +291,32 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void ragged_gemm_kernel(RaggedArgs
   };
 
   if (steps > 0) {
-    fetch(lds0);
-    vm_wait<0>();
+    uint32_t a0 = lds0, b0 = a0 + kSlot, a1 = b0 + kSlot, b1 = a1 + kSlot, a2 = b1 + kSlot;
+    fetch(a0, b0);
+    fetch(a1, b1);
+    vm_wait<OA::NI + OB::NI>();
     barrier_only();
-    fetch(lds0 + kStage);
-    load(lds0, 0);
+#pragma unroll
+    for (int i = 0; i < TM; ++i) ra[0][i] = fa.read(a0, i, 0);
+#pragma unroll
+    for (int j = 0; j < TN; ++j) rb[0][j] = fb.read(b0, j, 0);
     lgkm_wait0();
-    uint32_t cur = lds0, other = lds0 + kStage;
     for (int s = 0; s < steps; ++s) {
-      half_step(std::integral_constant<int, 0>{}, cur, std::false_type{}, 0u);
+      // first half: its fragments are in registers; A(s + 2) follows into its slot
+      next_a();
+      half_step(std::integral_constant<int, 0>{}, a0, b0, a2);
       lgkm_wait0();
-      vm_wait<0>();    // this wave's share of the next step has landed
-      barrier_only();  // everyone's has, and nobody reads `cur` any more
-      next_step();
-      half_step(std::integral_constant<int, 1>{}, other, std::true_type{}, cur);  // after the last step: stale values, not used
+      vm_wait<OA::NI>();  // this wave's share of step s + 1 has landed (that A(s + 2) may be under way)
+      barrier_only();     // everyone's has, and nobody reads a0 and b0 any more: B(s + 2), then A(s + 3)
+      next_b();
+      half_step(std::integral_constant<int, 1>{}, a1, b1, a0);  // reads of the step after the last: not used
       lgkm_wait0();
-      const uint32_t t = cur;
-      cur = other;
-      other = t;
+      const uint32_t was_a = a0, was_b = b0;
+      a0 = a1;
+      b0 = b1;
+      a1 = a2;
+      b1 = was_a;
+      a2 = was_b;
     }
     vm_wait<0>();
   }
