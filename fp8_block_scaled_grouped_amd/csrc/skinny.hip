@@ -50,14 +50,42 @@ __device__ __forceinline__ void swap16(uint32_t& a, uint32_t& b) {
   b = r[1];
 }
 
+// Rotation of the scales of row r in LDS, rows of 2^sh dwords: 16 rows' scales of one group in different banks.
+__device__ __forceinline__ int scale_swz(int r, int sh) { return (r & 15) >> (sh < 6 ? 6 - sh : 0); }
+
 // LDS-DMA of a dword per lane.
 __device__ __forceinline__ void dma4_buf(u32x4 rsrc, uint32_t off, uint32_t m0) {
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds" ::"v"(off), "s"(rsrc), "s"(m0)
                : "memory");
 }
 
-// LDS-DMA of COUNT KB as rows of RC 16-byte chunks, chunk c of row r in slot c ^ (r & MASK).
-template <int COUNT, int RC, int MASK>
+// Chunk c of row r lies in slot c ^ S(r), so that the 16 lanes that the LDS serves at a time (lanes 0-3 and
+// 12-15 of one lane group with 4-11 of the next, or the rest of the two) find their 16-byte chunks in
+// different banks.  S is linear: S(a | b) = S(a) ^ S(b) for rows a, b without common bits.
+//
+// Weights: lane group g reads chunk .. + g of rows 0 to 15; RC chunks a row.
+template <int RC>
+struct WeightSlots {
+  static __device__ __forceinline__ int of(int r) {
+    if constexpr (RC >= 16) return r & 15;
+    if constexpr (RC == 8) return r & 7;      // two rows a bank round
+    const int q = (r >> 2) & 3;               // four rows a bank round
+    return ((q << 1) & 2) ^ ((q >> 1) * 3);
+  }
+};
+// x: lane group g reads chunk .. + STEP g of rows 0 to min(ROWS, 16) - 1, which repeat.
+template <int ROWS, int STEP>
+struct XSlots {
+  static __device__ __forceinline__ int of(int r) {
+    if constexpr (STEP == 1) return (ROWS < 16 ? r << 1 : r) & 15;
+    if constexpr (ROWS <= 4) return r & 3;
+    if constexpr (ROWS == 8) return (r & 3) | ((r & 4) << 1);
+    return ((r & 3) << 2) | ((r >> 2) & 3);
+  }
+};
+
+// LDS-DMA of COUNT KB as rows of RC 16-byte chunks, swizzled by SLOTS.
+template <int COUNT, int RC, class SLOTS>
 struct RowCopy {
   static constexpr int kRows = RC < 64 ? 64 / RC : 1;   // rows of a DMA instruction
   static constexpr int kParts = RC < 64 ? 1 : RC / 64;  // instructions of a row
@@ -67,7 +95,7 @@ struct RowCopy {
   __device__ __forceinline__ void init(int lane, int64_t stride) {
     const int r = RC < 64 ? lane / RC : 0;
     base = (uint32_t)(r * stride);
-    chunk = (RC < 64 ? lane % RC : lane) ^ (r & MASK);
+    chunk = (RC < 64 ? lane % RC : lane) ^ SLOTS::of(r);
   }
   // TAIL: chunks of `left` and more read zeros;
   // and only instructions `part`, part + PARTS, ... are this wave's.
@@ -81,7 +109,7 @@ struct RowCopy {
     asm volatile("" : "+v"(base), "+v"(chunk));
 #pragma unroll
     for (int i = 0; i < COUNT / PARTS; ++i) {
-      const int j = i * PARTS + part, row = j / kParts * kRows, c = (chunk ^ (row & MASK)) + j % kParts * 64;
+      const int j = i * PARTS + part, row = j / kParts * kRows, c = (chunk ^ SLOTS::of(row)) + j % kParts * 64;
       const uint32_t off = base + row * stride + c * 16;
       dma16_buf(rsrc, TAIL && c >= left ? kPastEnd : off, dst + j * 1024);
     }
@@ -99,9 +127,11 @@ struct Format {
   static constexpr int kFolds = 4 / kPerScale;              // folds of a block
   static constexpr int kScaleBytes = W == kFp4 ? 4 : 1;
 
+  static constexpr bool kNatural = W == kW16 || (kFold && GROUP == 32);  // lane group g reads x's chunk 4 i + g
+
   // 8-wide chunk of x's block that goes with operand i of lane group g
   static __device__ __forceinline__ int xchunk(int i, int g) {
-    if constexpr (W == kW16 || (kFold && GROUP == 32)) return 4 * i + g;
+    if constexpr (kNatural) return 4 * i + g;
     if constexpr (kFold && GROUP == 64) return 8 * (i >> 1) + (i & 1) + 4 * (g & 1) + 2 * (g >> 1);
     return 4 * g + i;
   }
@@ -128,7 +158,8 @@ struct Skinny {
   static constexpr int NW = CW * KW, NC = 16 * CT * CW;
   static constexpr int kK = 128 * H * KW;                       // k of a stage
   static constexpr int kRowChunks = KW * H * Fm::kChunks;       // of a weight row in a stage
-  static constexpr int kWMask = kRowChunks < 16 ? kRowChunks - 1 : 15;  // of the weights' swizzle
+  using WSlots = WeightSlots<kRowChunks>;
+  using RowSlots = XSlots<MR, Fm::kNatural ? 1 : 4>;
   static constexpr int kWBytes = NC * kRowChunks * 16;          // weights of a stage
   static constexpr int kXBytes = MR * kK * 2;
   static constexpr int kStage = kWBytes + kXBytes;
@@ -194,8 +225,8 @@ __global__ __launch_bounds__((CW * KW + NP) * 64) void skinny_kernel(SkinnyArgs 
       const uint8_t* xp = reinterpret_cast<const uint8_t*>(a.x + (int64_t)m0 * a.ldx) + (int64_t)s0 * Sk::kK * 2;
       int64_t wlen = cols * rowbytes - (int64_t)s0 * Sk::kRowChunks * 16;
       int64_t xlen = ((int64_t)(rows - 1) * a.ldx + a.K) * 2 - (int64_t)s0 * Sk::kK * 2;
-      RowCopy<Sk::kDmaW, Sk::kRowChunks, Sk::kWMask> wc;
-      RowCopy<Sk::kDmaX, Sk::kK / 8, 15> xc;
+      RowCopy<Sk::kDmaW, Sk::kRowChunks, typename Sk::WSlots> wc;
+      RowCopy<Sk::kDmaX, Sk::kK / 8, typename Sk::RowSlots> xc;
       wc.init(lane, rowbytes);
       xc.init(lane, a.ldx * 2);
       auto fetch = [&](int s) {
@@ -212,13 +243,13 @@ __global__ __launch_bounds__((CW * KW + NP) * 64) void skinny_kernel(SkinnyArgs 
         }
         if constexpr (W != kW16) {
           if ((s == s0 || s % Sk::kWindowStages == 0) && !loose) {
-            // dword i of the window: row i / (dwords of a row); dwords past the row's end are zeros
+            // dword i of the window: row i / (dwords of a row), swizzled; dwords past the row's end are zeros
             const int q = s / Sk::kWindowStages, sh = 31 - __builtin_clz(slots * Fm::kScaleBytes / 4);
             const int first = q * Sk::kWindow * Fm::kScaleBytes;
             const u32x4 sd = dma_buffer(scales, cols * srowbytes);
             const uint32_t win = lds_scale + (q & 1) * window;
             for (int i0 = 64 * part; i0 < (Sk::NC << sh); i0 += 64 * NP) {
-              const int i = i0 + lane, r = i >> sh, at = first + (i - (r << sh)) * 4;
+              const int i = i0 + lane, r = i >> sh, at = first + ((i - (r << sh)) ^ scale_swz(r, sh)) * 4;
               if (i < Sk::NC << sh)
                 dma4_buf(sd, at < srowbytes ? (uint32_t)r * (uint32_t)srowbytes + at : kPastEnd, win + i0 * 4);
             }
@@ -252,11 +283,12 @@ __global__ __launch_bounds__((CW * KW + NP) * 64) void skinny_kernel(SkinnyArgs 
 #pragma unroll
         for (int i = 0; i < Fm::kLoads; ++i)
           wat[h][i] = (cw * CT * 16 + r) * (Sk::kRowChunks * 16) +
-                      ((((kw * H + h) * Fm::kChunks + 4 * i + g) ^ (r & Sk::kWMask)) << 4);
+                      ((((kw * H + h) * Fm::kChunks + 4 * i + g) ^ Sk::WSlots::of(r)) << 4);
       const int xr = r & (MR < 16 ? MR - 1 : 15);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        xat[i] = Sk::kWBytes + xr * (Sk::kK * 2) + ((kw * H * 16 + (Fm::xchunk(i, g) ^ (xr & 15))) << 4);
+        xat[i] = Sk::kWBytes + xr * (Sk::kK * 2) + ((kw * H * 16 + (Fm::xchunk(i, g) ^ Sk::RowSlots::of(xr))) << 4);
+      const int swz = scale_swz(r, 31 - __builtin_clz(slots * Fm::kScaleBytes / 4)) * (4 / Fm::kScaleBytes);
       // the lane's column, the wave's first group of a stage; E8M0 in the conversion: the lane's own group
       const int col = cw * CT * 16 + r;
       const int sgroup = kw * H * 128 / GROUP + (Fm::kDirect ? 32 * g / GROUP : 0);
@@ -280,10 +312,10 @@ __global__ __launch_bounds__((CW * KW + NP) * 64) void skinny_kernel(SkinnyArgs 
         auto scale_of = [&](int c, int at) -> uint32_t {                   // of tile c, group `at` on from sgroup
           const int row = col + 16 * c;
           if constexpr (W == kFp4) {
-            return *reinterpret_cast<pu>(win + (row * slots + sw + at) * 4);
+            return *reinterpret_cast<pu>(win + (row * slots + ((sw + at) ^ swz)) * 4);
           } else {
             if (loose) return scales[min(row, cols - 1) * srowbytes + min(s * (Sk::kK / GROUP) + sgroup + at, G - 1)];
-            return *reinterpret_cast<pb>(win + row * slots + sw + at);
+            return *reinterpret_cast<pb>(win + row * slots + ((sw + at) ^ swz));
           }
         };
 #pragma unroll
