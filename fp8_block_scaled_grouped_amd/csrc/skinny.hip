@@ -427,8 +427,14 @@ int launch_tile(SkinnyArgs g, hipStream_t stream) {
   return launch_status();
 }
 
-// One matrix, more than 16 rows: 128 columns a workgroup where that gives half of the CUs one.
-bool skinny_wide(int64_t M, int64_t N) { return ceil_div64(N, 128) * ceil_div64(M, M <= 32 ? 32 : 64) >= 128; }
+// Columns of a workgroup for one matrix of more than 16 rows: 128 where that gives half of the CUs one.  Else
+// K is split over workgroups (skinny_splits): 64 columns above 32 rows where there are many columns and a
+// long K, else 32.
+int skinny_cols(int64_t M, int64_t N, int64_t K) {
+  const int64_t passes = ceil_div64(M, M <= 32 ? 32 : 64);
+  if (ceil_div64(N, 128) * passes >= 128) return 128;
+  return M > 32 && K > 4096 && ceil_div64(N, 64) * passes >= 64 ? 64 : 32;
+}
 
 // The tiling of a launch.  Rows of a pass (MR): the rows of a matrix, of an expert on average; one that
 // has more takes another pass over weights that the caches still hold.  Columns of a workgroup: as many
@@ -436,13 +442,17 @@ bool skinny_wide(int64_t M, int64_t N) { return ceil_div64(N, 128) * ceil_div64(
 //   1 row, 2048 x 7168:      16 columns 6.4, 32 columns 9.2
 //   1 row, 18432 x 7168:     32 columns 15.7, 16 16.3, 64 17.2
 //   8 rows, 4096 x 7168:     8 rows a pass 7.8, 16 8.4
-//   16 rows, 18432 x 7168:   32 columns 19.9 (one block a stage; two 20.6), 128 columns 21.5
-//   32 rows, 18432 x 7168:   128 columns with K in two 21.8, K in one 25.1
-//   64 rows, 18432 x 7168:   128 columns with K in two 35.4, 256 columns and 3 runs of K 36.5
-//   64 rows, 2048 x 7168:    64 columns and 7 runs of K 13.3, 1 run 25.2
+//   16 rows, 18432 x 7168:   32 columns in two stages of two blocks 25.0, four of one 27.4 (E8M0);
+//                            128 columns 19.2, 32 22.0 (fp32 scales)
+//   32 rows, 18432 x 7168:   128 columns with K in two 24.2, K in one 26.7
+//   32 rows, 4096 x 7168:    32 columns and 2 runs of K 11.6, 64 and 4 12.1
+//   64 rows, 18432 x 7168:   128 columns with K in two 35.3, 256 columns and 3 runs of K 38.8
+//   64 rows, 7168 x 18432:   64 columns and 2 runs of K 36.3, four copying waves 38.5, 32 columns and 1 run 47
+//   64 rows, 2048 x 7168:    32 columns and 4 runs of K 11.7, 64 and 7 12.9, 32 and 1 18
+//   48 rows, 7168 x 2048:    32 columns 8.5, 64 and 2 runs of K 11.4
 //   one token's 8 experts of 4096 x 7168: 64 columns 34.0, 128 38.1
-//   64 tokens, top-8 of 256 experts of 7168 x 2048: 128 columns 283, 64 324; of 4096 x 7168: 577, 575
-//   2048 rows over 64 experts of 4096 x 7168: 64 rows a pass 297, 32 388
+//   64 tokens, top-8 of 256 experts of 7168 x 2048: 128 columns 295, 64 324; of 4096 x 7168: 577, 575
+//   2048 rows over 64 experts of 4096 x 7168: 64 rows a pass and 256 columns 283, 128 292; 32 rows 388
 template <int W, int GROUP, bool F16>
 int launch(const SkinnyArgs& g, hipStream_t stream) {
   constexpr int H = W == kW16 ? 1 : 2;  // 4-bit rows: whole 128-byte lines
@@ -466,26 +476,31 @@ int launch(const SkinnyArgs& g, hipStream_t stream) {
     if (groups(128) >= 1024) return launch_tile<W, GROUP, F16, 16, 2, 4, 1, H, 3, 4>(g, stream);
     if (groups(64) >= 512) return launch_tile<W, GROUP, F16, 16, 2, 2, 2, 1, 3, 4>(g, stream);
     if (groups(32) < 192) return launch_tile<W, GROUP, F16, 16, 1, 1, 4, H, 3, 4>(g, stream);
-    return launch_tile<W, GROUP, F16, 16, 1, 2, 2, 1, 4, 2>(g, stream);
+    if constexpr (W == kFp4 && GROUP == 128) {  // the fewest scales: 128 columns' fit beside the stages
+      if (groups(128) >= 128) return launch_tile<W, GROUP, F16, 16, 2, 4, 2, H, 3, 4>(g, stream);
+    }
+    return launch_tile<W, GROUP, F16, 16, 1, 2, 2, H, W == kW16 ? 3 : 2, W == kW16 ? 2 : 4>(g, stream);
   }
   if constexpr (W == kW16) return MOE355_EUNSUPPORTED;  // more rows are the tiled product's
   if constexpr (W != kW16) {
     if (g.offsets) {
-      if (rows <= 20) return launch_tile<W, GROUP, F16, 32, 2, 4, 1, 1, 4, 4>(g, stream);
-      if constexpr (W == kFp4 && GROUP == 32) {  // 256 columns' scales do not fit
-        return launch_tile<W, GROUP, F16, 64, 2, 4, 1, 1, 3, 4>(g, stream);
+      if (rows <= 20) return launch_tile<W, GROUP, F16, 32, 2, 4, 1, 2, 2, 4>(g, stream);
+      // 256 columns' fp32 scales of 32 or 64 do not fit, and folding them in fp16 takes too many registers
+      if constexpr ((W == kFp4 && GROUP == 128) || (W == kFp4E8M0 && !F16)) {
+        return launch_tile<W, GROUP, F16, 64, 2, 8, 1, 2, 2, 4>(g, stream);
       } else {
-        return launch_tile<W, GROUP, F16, 64, 4, 4, 1, 1, 3, 4>(g, stream);
+        return launch_tile<W, GROUP, F16, 64, 2, 4, 1, 1, 3, 4>(g, stream);
       }
     }
-    const bool wide = skinny_wide(g.R, g.N);
+    const int cols = skinny_cols(g.R, g.N, g.K);
     if (rows <= 32) {
-      if (wide) return launch_tile<W, GROUP, F16, 32, 2, 4, 2, 1, 3, 8>(g, stream);
-      return launch_tile<W, GROUP, F16, 32, 1, 4, 2, 1, 3, 4>(g, stream);
+      if (cols == 128) return launch_tile<W, GROUP, F16, 32, 2, 4, 2, 1, 3, 8>(g, stream);
+      return launch_tile<W, GROUP, F16, 32, 1, 2, 2, 2, 3, 4>(g, stream);
     }
     constexpr int S = W == kFp4 && GROUP < 128 ? 2 : 3;  // three stages and the fp32 scales do not fit
-    if (wide) return launch_tile<W, GROUP, F16, 64, 2, 4, 2, 1, S, 4>(g, stream);
-    return launch_tile<W, GROUP, F16, 64, 1, 4, 2, 1, 3, 4>(g, stream);
+    if (cols == 128) return launch_tile<W, GROUP, F16, 64, 2, 4, 2, 1, S, 4>(g, stream);
+    if (cols == 64) return launch_tile<W, GROUP, F16, 64, 1, 4, 2, 1, 3, 8>(g, stream);
+    return launch_tile<W, GROUP, F16, 64, 1, 2, 2, 1, 3, 4>(g, stream);
   }
 }
 
@@ -501,9 +516,10 @@ int by_group(const SkinnyArgs& g, int group, hipStream_t stream) {
 }  // namespace
 
 int skinny_splits(int M, int N, int K) {
-  if (M <= 16 || skinny_wide(M, N)) return 1;
-  // 64 columns a workgroup: as many runs of K, of at least 1024, as give each of the 256 CUs one
-  const int64_t tiles = ceil_div64(N, 64) * ceil_div64(M, M <= 32 ? 32 : 64), runs = ceil_div64(K, 1024);
+  const int cols = skinny_cols(M, N, K);
+  if (M <= 16 || cols == 128) return 1;
+  // as many runs of K, of at least 1024, as give each of the 256 CUs a workgroup
+  const int64_t tiles = ceil_div64(N, cols) * ceil_div64(M, M <= 32 ? 32 : 64), runs = ceil_div64(K, 1024);
   const int64_t s = tiles >= 256 ? 1 : 256 / tiles;
   return (int)(s < runs ? s : runs);
 }
