@@ -13,7 +13,8 @@
 //
 // A lane takes 16 bytes of a weight row's 128-wide block: 32 codes, k [32 g, 32 g + 32) for
 // lane group g = lane / 16.  The conversion instruction turns 8 codes into an operand in 4
-// issues.  E8M0 scales with bf16 x go into the conversion itself (exact).  Else the scale
+// issues.  E8M0 scales with bf16 x go into the conversion itself (exact), with fp16 x those of 32
+// relative to the largest of a block (Format::kRelative).  Else the scale
 // multiplies the fp32 tile of its group, so an MFMA's 32 k must lie in one group: groups of
 // 128 take any order, for groups of 64 and 32 the lanes of a column exchange codes first (one
 // or two lane-swap steps), and x is read in the order that results.
@@ -22,9 +23,9 @@
 // descriptors: they arrive as zeros, without traffic.
 //
 // Measured (18432 x 7168, fp32 scales of 128): 1 row 15.5 us (4.5 TB/s of weights and scales;
-// fragment-shaped register loads 31 us), 16 rows 22 us; 64 tokens through 222 of 256 experts of
-// 7168 x 2048 302 us (5.8 TB/s; 497 us).  A single copying wave issues too slowly for a CU's share
-// of the stream: with two, 1 row over 2048 x 7168 takes 6.8 us instead of 8.4, with 64 rows four
+// fragment-shaped register loads 31 us), 16 rows 19 us, 64 rows 35 us; 64 tokens through 222 of 256
+// experts of 7168 x 2048 290 us (6.0 TB/s; 497 us).  A single copying wave issues too slowly for a CU's
+// share of the stream: with two, 1 row over 2048 x 7168 takes 6.8 us instead of 8.4, with 64 rows four
 // take 33 us where one takes 46.
 #include "skinny.h"
 
@@ -123,20 +124,27 @@ struct Format {
   static constexpr int kChunks = W == kW16 ? 16 : 4;        // 16-byte chunks of a row's 128-wide block
   static constexpr int kPerChunk = W == kW16 ? 8 : 32;      // k of a chunk
   static constexpr int kLoads = W == kW16 ? 4 : 1;          // chunks a lane reads per 128-wide block
-  static constexpr int kPerScale = kFold ? GROUP / 32 : 4;  // MFMAs that share a fold
-  static constexpr int kFolds = 4 / kPerScale;              // folds of a block
+  // fp16 products with E8M0 scales of 32, four in a block: the conversion takes a scale relative to the
+  // block's largest and the fold that one.  Relative scales of at least 2^-13 keep e2m1's values (from 0.5 on)
+  // normal in fp16, so exact; a wave that holds a smaller one folds that block's groups one by one.  Four folds
+  // a block for all instead: 64 rows, 18432 x 7168, 106 us (42 now); 16 rows 25.0 (22.0); 1 row 22.9 (18.9).
+  static constexpr bool kRelative = W == kFp4E8M0 && F16 && GROUP == 32;
+  static constexpr int kSpread = 13;
+  static constexpr int kPerScale = kFold && !kRelative ? GROUP / 32 : 4;  // MFMAs that share a fold
+  static constexpr int kFolds = 4 / kPerScale;                            // folds of a block
   static constexpr int kScaleBytes = W == kFp4 ? 4 : 1;
 
-  static constexpr bool kNatural = W == kW16 || (kFold && GROUP == 32);  // lane group g reads x's chunk 4 i + g
+  static constexpr bool kMixed = kFold && !kRelative && GROUP < 128;  // an operand holds one group's codes
+  static constexpr bool kNatural = W == kW16 || (kMixed && GROUP == 32);  // lane group g reads x's chunk 4 i + g
 
   // 8-wide chunk of x's block that goes with operand i of lane group g
   static __device__ __forceinline__ int xchunk(int i, int g) {
     if constexpr (kNatural) return 4 * i + g;
-    if constexpr (kFold && GROUP == 64) return 8 * (i >> 1) + (i & 1) + 4 * (g & 1) + 2 * (g >> 1);
+    if constexpr (kMixed && GROUP == 64) return 8 * (i >> 1) + (i & 1) + 4 * (g & 1) + 2 * (g >> 1);
     return 4 * g + i;
   }
   static __device__ __forceinline__ void arrange(u32x4& q) {
-    if constexpr (kFold && GROUP <= 64) {
+    if constexpr (kMixed) {
       uint32_t d[4] = {q[0], q[1], q[2], q[3]};
       swap32(d[0], d[2]);
       swap32(d[1], d[3]);
@@ -318,6 +326,13 @@ __global__ __launch_bounds__((CW * KW + NP) * 64) void skinny_kernel(SkinnyArgs 
             return *reinterpret_cast<pb>(win + row * slots + ((sw + at) ^ swz));
           }
         };
+        auto scales_of = [&](int c, int at) -> uint32_t {  // E8M0 of 32: the four of a block, a byte each
+          const int row = col + 16 * c;
+          if (!loose) return *reinterpret_cast<pu>(win + row * slots + ((sw + at) ^ swz));
+          uint32_t v = 0;
+          for (int j = 0; j < 4; ++j) v |= scale_of(c, at + j) << 8 * j;
+          return v;
+        };
 #pragma unroll
         for (int h = 0; h < H; ++h) {
           s16x8 x[MT][4];
@@ -334,18 +349,46 @@ __global__ __launch_bounds__((CW * KW + NP) * 64) void skinny_kernel(SkinnyArgs 
             uint32_t sv[Fm::kFolds];
             if constexpr (W != kW16) {
 #pragma unroll
-              for (int i = 0; i < Fm::kFolds; ++i) sv[i] = scale_of(c, h * (128 / GROUP) + i);
+              for (int i = 0; i < Fm::kFolds && !Fm::kRelative; ++i) sv[i] = scale_of(c, h * (128 / GROUP) + i);
               Fm::arrange(q[0]);
             }
             v4f tile[MT];
+            float conv = 1.0f;  // the conversion reads the scale's exponent field (0 as 2^-127)
+            if constexpr (Fm::kDirect) conv = __uint_as_float(sv[0] << 23);
+            if constexpr (Fm::kRelative) {
+              const uint32_t all = scales_of(c, 4 * h);
+              sv[0] = max(max(all & 255, all >> 8 & 255), max(all >> 16 & 255, all >> 24));
+              const uint32_t below = sv[0] - (all >> 8 * g & 255);
+              conv = __uint_as_float((127 - below) << 23);
+              if (__any(below > Fm::kSpread)) {  // rare: each group by itself, the other lanes' x and codes zero
+#pragma unroll 1
+                for (int j = 0; j < 4; ++j) {
+                  const bool mine = g == j;
+                  const float scale = e8m0_to_f32(all >> 8 * j & 255);
+#pragma unroll
+                  for (int t = 0; t < MT; ++t) {
+                    tile[t] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                      uint32_t codes = mine ? q[0][i] : 0u;
+                      asm volatile("" : "+v"(codes));  // converted anew for each t: no registers to keep it in
+                      tile[t] = mfma16x16x32<F16>(mine ? x[t][i] : s16x8{}, e2m1x8<F16>(codes, 1.0f), tile[t]);
+                      __builtin_amdgcn_sched_barrier(0);
+                    }
+                    acc[t][c] += tile[t] * scale;
+                  }
+                }
+                continue;
+              }
+            }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               s16x8 b;
               if constexpr (W == kW16) {
                 const u32x4 v = q[i];
                 b = __builtin_bit_cast(s16x8, v);
-              } else {  // the conversion reads the scale's exponent field (0 as 2^-127)
-                b = e2m1x8<F16>(q[0][i], Fm::kDirect ? __uint_as_float(sv[0] << 23) : 1.0f);
+              } else {
+                b = e2m1x8<F16>(q[0][i], conv);
               }
               const bool first = i % Fm::kPerScale == 0, last = i % Fm::kPerScale == Fm::kPerScale - 1;
 #pragma unroll
@@ -442,7 +485,7 @@ int skinny_cols(int64_t M, int64_t N, int64_t K) {
 //   1 row, 2048 x 7168:      16 columns 6.4, 32 columns 9.2
 //   1 row, 18432 x 7168:     32 columns 15.7, 16 16.3, 64 17.2
 //   8 rows, 4096 x 7168:     8 rows a pass 7.8, 16 8.4
-//   16 rows, 18432 x 7168:   32 columns in two stages of two blocks 25.0, four of one 27.4 (E8M0);
+//   16 rows, 18432 x 7168:   32 columns in two stages of two blocks 22.2, 64 24.0 (E8M0);
 //                            128 columns 19.2, 32 22.0 (fp32 scales)
 //   32 rows, 18432 x 7168:   128 columns with K in two 24.2, K in one 26.7
 //   32 rows, 4096 x 7168:    32 columns and 2 runs of K 11.6, 64 and 4 12.1
@@ -450,8 +493,9 @@ int skinny_cols(int64_t M, int64_t N, int64_t K) {
 //   64 rows, 7168 x 18432:   64 columns and 2 runs of K 36.3, four copying waves 38.5, 32 columns and 1 run 47
 //   64 rows, 2048 x 7168:    32 columns and 4 runs of K 11.7, 64 and 7 12.9, 32 and 1 18
 //   48 rows, 7168 x 2048:    32 columns 8.5, 64 and 2 runs of K 11.4
-//   one token's 8 experts of 4096 x 7168: 64 columns 34.0, 128 38.1
-//   64 tokens, top-8 of 256 experts of 7168 x 2048: 128 columns 295, 64 324; of 4096 x 7168: 577, 575
+//   one token's 8 experts of 4096 x 7168: 64 columns with K in two 34.5, in one 36.6, 128 columns 38.1
+//   512 rows over 256 experts: of 7168 x 2048, 16 rows a pass and 128 columns 282, 8 and 64 304;
+//                              of 4096 x 7168, 8 rows a pass and 64 columns 572, 16 and 128 632
 //   2048 rows over 64 experts of 4096 x 7168: 64 rows a pass and 256 columns 283, 128 292; 32 rows 388
 template <int W, int GROUP, bool F16>
 int launch(const SkinnyArgs& g, hipStream_t stream) {
@@ -466,14 +510,25 @@ int launch(const SkinnyArgs& g, hipStream_t stream) {
       return launch_tile<W, GROUP, F16, 4, 1, 2, 2, H, 3, 2>(g, stream);
     }
   }
-  if (rows <= (g.offsets ? 4 : 8)) {
-    if (groups(128) >= 1024) return launch_tile<W, GROUP, F16, 8, 2, 4, 1, H, 3, W == kW16 ? 2 : 4>(g, stream);
+  const bool wide = groups(128) >= 1024;
+  // over a short K another pass for the experts of more than 8 rows costs more than wider passes for all
+  const bool at_once = W != kW16 && g.offsets && wide && g.K < 4096;
+  if (rows <= (g.offsets ? 4 : 8) && !at_once) {
+    if constexpr (W == kW16) {
+      if (wide) return launch_tile<W, GROUP, F16, 8, 2, 4, 1, 1, 3, 2>(g, stream);
+    } else {
+      if (wide) return launch_tile<W, GROUP, F16, 8, 1, 4, 1, H, 3, 4>(g, stream);
+    }
     if (groups(64) >= 512) return launch_tile<W, GROUP, F16, 8, 2, 2, 2, H, W == kW16 ? 4 : 3, 2>(g, stream);
     if (groups(32) < 192) return launch_tile<W, GROUP, F16, 8, 1, 1, 4, H, 3, 4>(g, stream);
     return launch_tile<W, GROUP, F16, 8, 1, 2, 2, H, 3, 2>(g, stream);
   }
   if (rows <= (g.offsets ? 12 : 16)) {
-    if (groups(128) >= 1024) return launch_tile<W, GROUP, F16, 16, 2, 4, 1, H, 3, 4>(g, stream);
+    if constexpr (W == kW16) {
+      if (wide) return launch_tile<W, GROUP, F16, 16, 2, 4, 1, 1, 3, 4>(g, stream);
+    } else {
+      if (wide) return launch_tile<W, GROUP, F16, 16, 4, 2, 2, 1, 3, 4>(g, stream);
+    }
     if (groups(64) >= 512) return launch_tile<W, GROUP, F16, 16, 2, 2, 2, 1, 3, 4>(g, stream);
     if (groups(32) < 192) return launch_tile<W, GROUP, F16, 16, 1, 1, 4, H, 3, 4>(g, stream);
     if constexpr (W == kFp4 && GROUP == 128) {  // the fewest scales: 128 columns' fit beside the stages
@@ -485,8 +540,8 @@ int launch(const SkinnyArgs& g, hipStream_t stream) {
   if constexpr (W != kW16) {
     if (g.offsets) {
       if (rows <= 20) return launch_tile<W, GROUP, F16, 32, 2, 4, 1, 2, 2, 4>(g, stream);
-      // 256 columns' fp32 scales of 32 or 64 do not fit, and folding them in fp16 takes too many registers
-      if constexpr ((W == kFp4 && GROUP == 128) || (W == kFp4E8M0 && !F16)) {
+      // 256 columns' fp32 scales of 32 or 64 do not fit, and folding E8M0 of 64 or 128 takes too many registers
+      if constexpr (W == kFp4 ? GROUP == 128 : !F16 || GROUP == 32) {
         return launch_tile<W, GROUP, F16, 64, 2, 8, 1, 2, 2, 4>(g, stream);
       } else {
         return launch_tile<W, GROUP, F16, 64, 2, 4, 1, 1, 3, 4>(g, stream);
@@ -499,7 +554,8 @@ int launch(const SkinnyArgs& g, hipStream_t stream) {
     }
     constexpr int S = W == kFp4 && GROUP < 128 ? 2 : 3;  // three stages and the fp32 scales do not fit
     if (cols == 128) return launch_tile<W, GROUP, F16, 64, 2, 4, 2, 1, S, 4>(g, stream);
-    if (cols == 64) return launch_tile<W, GROUP, F16, 64, 1, 4, 2, 1, 3, 8>(g, stream);
+    constexpr int NP = Format<W, GROUP, F16>::kRelative ? 4 : 8;  // 16 waves leave its registers too few
+    if (cols == 64) return launch_tile<W, GROUP, F16, 64, 1, 4, 2, 1, 3, NP>(g, stream);
     return launch_tile<W, GROUP, F16, 64, 1, 2, 2, 1, 3, 4>(g, stream);
   }
 }

@@ -165,6 +165,33 @@ def test_gemm_fp4_tilings(m, dtype, group, fmt, N, K, rows):
             _close(m.gemm_fp4_groupscale(x.to(DEV), q, s, group, workspace=False), ref, mag, K, dtype, "no workspace")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("group", [32, 64])
+@pytest.mark.parametrize("spread", [12, 13, 14, 22])
+def test_gemm_fp4_scales_far_apart(m, dtype, group, spread):
+    # neighbouring groups' powers of two up to 2^spread apart, in some columns only; x lies in one group in
+    # some rows, so that the smallest scales' products are whole results
+    print("fp4 spread", dtype, group, spread, flush=True)
+    for N, K, rows in ((40, 1056, (1, 7, 16, 24, 64)), (33000, 160, (2, 9, 20, 64))):
+        rng = np.random.default_rng(spread)
+        q = rng.integers(0, 256, (N, K // 2), dtype=np.uint8)
+        G = -(-K // group)
+        s = np.full((N, G), 121, np.uint8)
+        s[::3] = 125 - rng.choice([0, spread // 2, spread], (len(s[::3]), G)).astype(np.uint8)
+        w = fp4.dequant_groups(q, s, group)
+        for M in rows:
+            x = _randn((M, K), dtype, M, 8.0)
+            for r in range(1, M, 2):
+                lo = r // 2 % G * group
+                x[r, :lo], x[r, lo + group:] = 0, 0
+            xf = _f64(x)
+            c = m.gemm_fp4_groupscale(x.to(DEV), torch.tensor(q, device=DEV), torch.tensor(s, device=DEV), group)
+            _close(c, xf @ w.T, np.abs(xf) @ np.abs(w).T, K, dtype, "%d x %d x %d" % (M, N, K))
+    x[1, 5] = float("inf")  # infinite where the weight is not zero, whatever the block's other scales
+    c = m.gemm_fp4_groupscale(x.to(DEV), torch.tensor(q, device=DEV), torch.tensor(s, device=DEV), group)
+    assert torch.equal(c[1].isnan().cpu(), torch.tensor(w[:, 5] == 0))
+
+
 def test_gemm_fp4_workspace(m):
     x, (q, s, _) = _randn((64, 8192), "bf16", 1).to(DEV), _packed((520, 8192), 64, "fp32", 2)
     n = m.gemm_fp4_groupscale_workspace(64, 520, 8192)
