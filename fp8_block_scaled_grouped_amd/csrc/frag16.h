@@ -26,7 +26,8 @@ __device__ __forceinline__ v4f mfma16x16x32(const s16x8& a, const s16x8& b, cons
 }
 
 // Eight e2m1 codes (4 bits each, lowest first) -> eight bf16 or fp16 values times 2^(scale's
-// exponent); every code is exact in both types, and so is the product in bf16.
+// exponent); every code is exact in both types, and so is the product in bf16 up to a scale of 2^125 (6 x 2^126
+// and more become infinities).
 template <bool F16>
 __device__ __forceinline__ s16x8 e2m1x8(uint32_t codes, float scale) {
   u32x4 r;
@@ -41,6 +42,21 @@ __device__ __forceinline__ s16x8 e2m1x8(uint32_t codes, float scale) {
     r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 2));
     r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 3));
   }
+  return __builtin_bit_cast(s16x8, r);
+}
+
+// Eight e2m1 codes -> eight bf16 values times a power of two from 2^-129 to 2^125, or NaN: exact too, subnormal
+// values (multiples of 2^-130) among them.
+__device__ __forceinline__ s16x8 e2m1x8_times(uint32_t codes, float scale) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  const f32x2 v[4] = {__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 0),
+                      __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 1),
+                      __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 2),
+                      __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 3)};
+  u32x4 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    r[i] = __float_as_uint(v[i][0] * scale) >> 16 | (__float_as_uint(v[i][1] * scale) & 0xffff0000u);
   return __builtin_bit_cast(s16x8, r);
 }
 

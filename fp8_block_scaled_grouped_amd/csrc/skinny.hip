@@ -13,8 +13,9 @@
 //
 // A lane takes 16 bytes of a weight row's 128-wide block: 32 codes, k [32 g, 32 g + 32) for
 // lane group g = lane / 16.  The conversion instruction turns 8 codes into an operand in 4
-// issues.  E8M0 scales with bf16 x go into the conversion itself (exact), with fp16 x those of 32
-// relative to the largest of a block (Format::kRelative).  Else the scale
+// issues.  E8M0 scales with bf16 x go into the conversion itself (exact up to a byte of 252; weights past bf16's
+// range are taken again as quarters after the loop), with fp16 x those of 32 relative to the largest of a
+// block (Format::kRelative).  Else the scale
 // multiplies the fp32 tile of its group, so an MFMA's 32 k must lie in one group: groups of
 // 128 take any order, for groups of 64 and 32 the lanes of a column exchange codes first (one
 // or two lane-swap steps), and x is read in the order that results.
@@ -407,6 +408,67 @@ __global__ __launch_bounds__((CW * KW + NP) * 64) void skinny_kernel(SkinnyArgs 
             if constexpr (Fm::kFold && MT * CT >= 8) __builtin_amdgcn_sched_barrier(0);  // and of one tile
           }
           __builtin_amdgcn_sched_barrier(0);  // keeps the operands of one block in registers at a time
+        }
+      }
+      if constexpr (Fm::kDirect) {
+        // Under a byte of 253 or 254 the larger e2m1 values leave bf16's range: such a weight arrived as an infinity,
+        // and none of its products left a finite sum.  If a sum is not finite and a byte is that large, the wave
+        // takes its sums again, from memory, with weights of a quarter (18432 x 7168: 1 row 15.8 us without the
+        // check and 15.9 with it, 64 rows 32.6 and 33.2; looking at each byte in the loop 19.0 and 36.5, for its
+        // branches between the conversions and the MFMAs).
+        float z = 0.0f;
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+          for (int c = 0; c < CT; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) z = __builtin_fmaf(acc[t][c][i], 0.0f, z);
+        if (__any(!(z == 0.0f))) {
+          const int kend = min(a.K, s1 * Sk::kK);
+          bool high = false;
+#pragma unroll 1
+          for (int k = s0 * Sk::kK + 32 * g; k < kend; k += 128)
+#pragma unroll 1
+            for (int n = col; n < min(cols, col + 16 * CT); n += 16) {
+              const uint32_t byte = scales[n * srowbytes + k / GROUP];
+              high |= byte == 253 || byte == 254;
+            }
+          if (__any(high)) {
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+#pragma unroll
+              for (int c = 0; c < CT; ++c) acc[t][c] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+            for (int j = 0; j < (s1 - s0) * H * 4; ++j) {
+              // 8 of the lane's 32 k of a block
+              const int b = j >> 2, k = (s0 + b / H) * Sk::kK + (kw * H + b % H) * 128 + 32 * g + 8 * (j & 3);
+              s16x8 x[MT];
+#pragma unroll
+              for (int t = 0; t < MT; ++t) {
+                x[t] = s16x8{};
+                if (16 * t + r < min(hi - m0, MR) && k < a.K)
+                  x[t] = *reinterpret_cast<const s16x8*>(a.x + (int64_t)(m0 + 16 * t + r) * a.ldx + k);
+              }
+#pragma unroll
+              for (int c = 0; c < CT; ++c) {
+                const int n = col + 16 * c;
+                uint32_t codes = 0;
+                float quarter = 0.0f;
+                if (n < cols && k < a.K) {
+                  codes = *reinterpret_cast<const uint32_t*>(a.w + (((int64_t)e * a.N + n0 + n) * a.K + k) / 2);
+                  quarter = e8m0_to_f32(scales[n * srowbytes + k / GROUP]) * 0.25f;
+                }
+                const s16x8 b8 = e2m1x8_times(codes, quarter);
+#pragma unroll
+                for (int t = 0; t < MT; ++t) acc[t][c] = mfma16x16x32<F16>(x[t], b8, acc[t][c]);
+                __builtin_amdgcn_sched_barrier(0);
+              }
+            }
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+#pragma unroll
+              for (int c = 0; c < CT; ++c) acc[t][c] *= 4.0f;
+          }
         }
       }
       barrier_only();  // every stage has been read: the tiles may overwrite them
