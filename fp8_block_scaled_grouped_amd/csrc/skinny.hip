@@ -225,11 +225,12 @@ __global__ __launch_bounds__((CW * KW + NP) * 64) void skinny_kernel(SkinnyArgs 
   const uint32_t lds0 = lds_addr(smem), lds_scale = lds0 + S * Sk::kStage;
   const uint32_t window = Sk::NC * slots * Fm::kScaleBytes;  // bytes
 
-  for (int m0 = lo + zrow * MR; m0 < hi; m0 += zrows * MR) {
+  const int passes = (hi - lo - 1) / MR + 1;  // counted from the segment: row numbers may come close to 2^31
+  for (int pass = zrow; pass < passes; pass += zrows) {
+    const int m0 = lo + pass * MR, rows = min(hi - m0, MR);
     if (w >= NW) {
       const int part = w - NW;
       const int64_t rowbytes = (int64_t)a.K * 16 / Fm::kPerChunk;
-      const int rows = min(hi - m0, MR);
       const uint8_t* wp = a.w + ((int64_t)e * a.N + n0) * rowbytes + (int64_t)s0 * Sk::kRowChunks * 16;
       const uint8_t* xp = reinterpret_cast<const uint8_t*>(a.x + (int64_t)m0 * a.ldx) + (int64_t)s0 * Sk::kK * 2;
       int64_t wlen = cols * rowbytes - (int64_t)s0 * Sk::kRowChunks * 16;
@@ -424,6 +425,9 @@ __global__ __launch_bounds__((CW * KW + NP) * 64) void skinny_kernel(SkinnyArgs 
 #pragma unroll
             for (int i = 0; i < 4; ++i) z = __builtin_fmaf(acc[t][c][i], 0.0f, z);
         if (__any(!(z == 0.0f))) {
+          int again = lane;
+          asm volatile("" : "+v"(again));  // the places below: not kept in registers through the loop above
+          const int g = again >> 4, r = again & 15, col = cw * CT * 16 + r;
           const int kend = min(a.K, s1 * Sk::kK);
           bool high = false;
 #pragma unroll 1
@@ -446,7 +450,7 @@ __global__ __launch_bounds__((CW * KW + NP) * 64) void skinny_kernel(SkinnyArgs 
 #pragma unroll
               for (int t = 0; t < MT; ++t) {
                 x[t] = s16x8{};
-                if (16 * t + r < min(hi - m0, MR) && k < a.K)
+                if (16 * t + r < rows && k < a.K)
                   x[t] = *reinterpret_cast<const s16x8*>(a.x + (int64_t)(m0 + 16 * t + r) * a.ldx + k);
               }
 #pragma unroll
@@ -488,8 +492,9 @@ __global__ __launch_bounds__((CW * KW + NP) * 64) void skinny_kernel(SkinnyArgs 
       const int n = n0 + (cc * CT + c) * 16 + (lane & 15);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int m = m0 + 16 * t + 4 * g + i;
-        if (m >= hi || m >= m0 + MR || n >= a.N) continue;
+        const int at = 16 * t + 4 * g + i;
+        if (at >= rows || n >= a.N) continue;
+        const int m = m0 + at;
         if (a.splits > 1) {
           a.part[((int64_t)split * a.R + m) * a.N + n] = s[i];
         } else {
