@@ -632,6 +632,8 @@ class _GroupedLinear(torch.autograd.Function):
     def backward(ctx, dy):
         x, w, offsets = ctx.saved_tensors
         dy = dy.contiguous()
+        if dy.data_ptr() % 16:  # a view into a larger gradient may start anywhere
+            dy = dy.clone()
         dx = grouped_gemm_dgrad(dy, w, offsets) if ctx.needs_input_grad[0] else None
         dw = grouped_gemm_wgrad(dy, x, offsets) if ctx.needs_input_grad[1] else None
         return dx, dw, None

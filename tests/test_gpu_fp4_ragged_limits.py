@@ -42,3 +42,15 @@ def test_segment_that_ends_near_2_to_31(m, first):
     assert bool((c[first - 4096:first] == 7).all())
     del x, c
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_gradient_that_starts_off_16_bytes(m, dtype):
+    # the backward of a concatenation hands grouped_linear a view of its gradient that starts 6 bytes in
+    g = torch.Generator().manual_seed(3)
+    x, w = (torch.randn(s, generator=g).to(dtype).to(DEV) for s in ((6, 16), (2, 24, 16)))
+    od, up = torch.tensor([0, 2, 6], dtype=torch.int32, device=DEV), torch.randn(6 * 24 + 3, generator=g).to(dtype).to(DEV)
+    tx, tw, head = x.clone().requires_grad_(), w.clone().requires_grad_(), torch.zeros(3, dtype=dtype, device=DEV, requires_grad=True)
+    torch.cat([head, m.grouped_linear(tx, tw, od).flatten()]).backward(up)
+    dy = up[3:].clone().view(6, 24)
+    assert torch.equal(tx.grad, m.grouped_gemm_dgrad(dy, w, od)) and torch.equal(tw.grad, m.grouped_gemm_wgrad(dy, x, od))
