@@ -525,11 +525,12 @@ int launch_tile(SkinnyArgs g, hipStream_t stream) {
   // a large grid of mostly empty workgroups would cost more than it gives.
   const int64_t side = 4096 / (nx * g.E) > 1 ? 4096 / (nx * g.E) : 1;
   const int64_t nz = (g.offsets ? (passes < side ? passes : side) : passes) * g.splits;
-  MOE355_CHECK(nx < (1ll << 31) && nz < 65536, MOE355_EUNSUPPORTED);
+  constexpr int kThreads = (CW * KW + NP) * 64;
+  MOE355_CHECK(nx * kThreads < (1ll << 32) && nz < 65536, MOE355_EUNSUPPORTED);  // threads of a launch
   auto* fn = &skinny_kernel<W, GROUP, F16, MR, CT, CW, KW, H, S, NP>;
   const int lds = Sk::lds_bytes(g.K), G = (g.K + GROUP - 1) / GROUP;
   const int loose = W == kFp4E8M0 && (G % 4 != 0 || (reinterpret_cast<uintptr_t>(g.scale) & 3u) != 0);
-  hipLaunchKernelGGL(fn, dim3((unsigned)nx, (unsigned)g.E, (unsigned)nz), dim3((CW * KW + NP) * 64), lds, stream, g,
+  hipLaunchKernelGGL(fn, dim3((unsigned)nx, (unsigned)g.E, (unsigned)nz), dim3(kThreads), lds, stream, g,
                      Sk::scale_slots(g.K), loose);
   if (g.splits > 1)
     hipLaunchKernelGGL(skinny_reduce_kernel<F16>, dim3((unsigned)ceil_div64((int64_t)g.R * g.N, 256)), dim3(256), 0,

@@ -384,8 +384,8 @@ int gemm_fp4_groupscale_workspace(int M, int N, int K, size_t* bytes);
  * q      [N, K/2] and scale [N, G] as fp4_quant_groups writes them.
  * c      [M, N] out, the type of x, row stride ldc >= N; fp32 sums, nearest even.  Every scale byte from 0 to 254
  *        holds; a column with a NaN scale is NaN.  Terms x * w past fp32's range may leave a sum that is not finite.
- * Any M (to 4 million) and N; the time is the weights' bytes up to about 64 rows, beyond that the weights are
- * read again for every 64 rows.  K % 32 == 0 and ld_x up to 2097152, else MOE355_EUNSUPPORTED.
+ * Any M (to 4 million) and N (to 500 million); the time is the weights' bytes up to about 64 rows, beyond that the
+ * weights are read again for every 64 rows.  K % 32 == 0 and ld_x up to 2097152, else MOE355_EUNSUPPORTED.
  * workspace  device memory of gemm_fp4_groupscale_workspace() bytes, 16-byte aligned (contents
  *            need no initialisation), or NULL: K is then not split (slower from 17 rows on).
  *            Given but too small: MOE355_EINVAL.
