@@ -225,12 +225,13 @@ __global__ __launch_bounds__((CW * KW + NP) * 64) void skinny_kernel(SkinnyArgs 
   const uint32_t lds0 = lds_addr(smem), lds_scale = lds0 + S * Sk::kStage;
   const uint32_t window = Sk::NC * slots * Fm::kScaleBytes;  // bytes
 
-  const int passes = (hi - lo - 1) / MR + 1;  // counted from the segment: row numbers may come close to 2^31
-  for (int pass = zrow; pass < passes; pass += zrows) {
-    const int m0 = lo + pass * MR, rows = min(hi - m0, MR);
+  // unsigned: a row number past the segment may exceed 2^31
+  const uint32_t end = hi;
+  for (uint32_t m0 = lo + zrow * MR; m0 < end; m0 += zrows * MR) {
     if (w >= NW) {
       const int part = w - NW;
       const int64_t rowbytes = (int64_t)a.K * 16 / Fm::kPerChunk;
+      const int rows = min((int)(end - m0), MR);
       const uint8_t* wp = a.w + ((int64_t)e * a.N + n0) * rowbytes + (int64_t)s0 * Sk::kRowChunks * 16;
       const uint8_t* xp = reinterpret_cast<const uint8_t*>(a.x + (int64_t)m0 * a.ldx) + (int64_t)s0 * Sk::kK * 2;
       int64_t wlen = cols * rowbytes - (int64_t)s0 * Sk::kRowChunks * 16;
@@ -319,12 +320,23 @@ __global__ __launch_bounds__((CW * KW + NP) * 64) void skinny_kernel(SkinnyArgs 
         const uint32_t st = lds0 + (s % S) * Sk::kStage;
         const uint32_t win = lds_scale + (s / Sk::kWindowStages & 1) * window;
         const int sw = s % Sk::kWindowStages * (Sk::kK / GROUP) + sgroup;  // slot in the window
+        // fp16 x with E8M0 scales of 64, 64 x 32 results a wave and 168 registers (more than 8 waves): what takes
+        // registers through the loop (without this 7 are spilled, one of them read back in each stage) is computed
+        // here, from values that the compiler must take for new.
+        constexpr bool kTight = W == kFp4E8M0 && Fm::kFolds > 1 && MT * CT >= 8 && NW + NP > 8;
+        int apart = loose;
+        uint32_t x0 = xat[0];
+        if constexpr (kTight) asm volatile("" : "+s"(apart), "+v"(x0));
         auto scale_of = [&](int c, int at) -> uint32_t {                   // of tile c, group `at` on from sgroup
           const int row = col + 16 * c;
           if constexpr (W == kFp4) {
             return *reinterpret_cast<pu>(win + (row * slots + ((sw + at) ^ swz)) * 4);
           } else {
-            if (loose) return scales[min(row, cols - 1) * srowbytes + min(s * (Sk::kK / GROUP) + sgroup + at, G - 1)];
+            if (apart) {
+              int from = min(row, cols - 1);
+              if constexpr (kTight) asm volatile("" : "+v"(from));
+              return scales[from * srowbytes + min(s * (Sk::kK / GROUP) + sgroup + at, G - 1)];
+            }
             return *reinterpret_cast<pb>(win + row * slots + ((sw + at) ^ swz));
           }
         };
@@ -341,7 +353,10 @@ __global__ __launch_bounds__((CW * KW + NP) * 64) void skinny_kernel(SkinnyArgs 
 #pragma unroll
           for (int t = 0; t < MT; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[t][i] = *reinterpret_cast<px>(st + xat[i] + h * 256 + t * 16 * (Sk::kK * 2));
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t from = kTight ? x0 ^ (Fm::xchunk(i, 0) << 4) : xat[i];
+              x[t][i] = *reinterpret_cast<px>(st + from + h * 256 + t * 16 * (Sk::kK * 2));
+            }
 #pragma unroll
           for (int c = 0; c < CT; ++c) {
             u32x4 q[Fm::kLoads];
@@ -450,7 +465,7 @@ __global__ __launch_bounds__((CW * KW + NP) * 64) void skinny_kernel(SkinnyArgs 
 #pragma unroll
               for (int t = 0; t < MT; ++t) {
                 x[t] = s16x8{};
-                if (16 * t + r < rows && k < a.K)
+                if (16 * t + r < min((int)(end - m0), MR) && k < a.K)
                   x[t] = *reinterpret_cast<const s16x8*>(a.x + (int64_t)(m0 + 16 * t + r) * a.ldx + k);
               }
 #pragma unroll
@@ -492,9 +507,8 @@ __global__ __launch_bounds__((CW * KW + NP) * 64) void skinny_kernel(SkinnyArgs 
       const int n = n0 + (cc * CT + c) * 16 + (lane & 15);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int at = 16 * t + 4 * g + i;
-        if (at >= rows || n >= a.N) continue;
-        const int m = m0 + at;
+        const uint32_t m = m0 + 16 * t + 4 * g + i;
+        if (m >= end || m >= m0 + MR || n >= a.N) continue;
         if (a.splits > 1) {
           a.part[((int64_t)split * a.R + m) * a.N + n] = s[i];
         } else {
