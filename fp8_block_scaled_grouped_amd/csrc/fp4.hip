@@ -48,7 +48,8 @@ __device__ __forceinline__ float quotient(float w, float s, float r, bool plain)
 
 // 8 values a lane; GROUP / 8 lanes own a group.  FLAT: rows of whole groups, one after the other, as one
 // row (no division to find their place).  Bound by memory: 2 K bytes in, K / 2 and the scales out a row;
-// 131072 x 7168 takes 0.40 ms with E8M0 scales of 32 (5.9 TB/s), 0.49 with fp32 scales of 128 (4.9 TB/s).
+// 131072 x 7168 takes 0.42 ms with E8M0 scales of 32 (5.7 TB/s; 0.43 to 0.46 between other calls), 0.50 with fp32
+// scales of 128 (4.8 TB/s).
 template <bool F16, bool E8M0, int GROUP, bool FLAT>
 __global__ __launch_bounds__(kThreads) void fp4_quant_kernel(const uint16_t* __restrict__ w, int64_t ld_w, int64_t rows,
                                                              int64_t K, int64_t G, uint8_t* __restrict__ q,

@@ -1,5 +1,5 @@
 // Products grouped by expert over ragged row segments, 16-bit operands: the
-// argument block and launch functions of ragged_gemm.hip.
+// argument block of ragged_gemm.hip's kernel.
 #pragma once
 
 #include <hip/hip_runtime.h>

@@ -4,12 +4,13 @@
 //   4-bit: c[m, n] = round(sum_g s[n, g] sum_{k in group g} x[m, k] q[n, k])
 //
 // The weights are read once and bound the time, so the kernel is built around their stream:
-// one wave of a workgroup does nothing but LDS-DMA, S stages deep, in whole 128-byte lines of
+// two to eight waves of a workgroup do nothing but LDS-DMA, S stages deep, in whole 128-byte lines of
 // the weight rows (fragment-shaped loads straight into registers, 16 rows x 64 bytes each,
 // ask for twice as many lines and the requests in flight, not the bytes, bounded them).  The
 // other waves multiply from LDS: 16 weight rows are an MFMA's columns, 16 rows of x its rows.  A
 // stage is 128 H k for each of KW waves that share columns; they add their fp32 tiles in LDS in
-// wave order at the end (deterministic, one launch, no workspace).
+// wave order at the end (deterministic, one launch, no workspace).  From 17 rows of one matrix on, where the columns
+// leave CUs idle, workgroups split K too: partial sums in a workspace, added by a second launch in order.
 //
 // A lane takes 16 bytes of a weight row's 128-wide block: 32 codes, k [32 g, 32 g + 32) for
 // lane group g = lane / 16.  The conversion instruction turns 8 codes into an operand in 4
@@ -23,11 +24,15 @@
 // Columns past N, rows past the segment and k past K lie past the end of the buffer
 // descriptors: they arrive as zeros, without traffic.
 //
-// Measured (18432 x 7168, fp32 scales of 128): 1 row 15.5 us (4.5 TB/s of weights and scales;
-// fragment-shaped register loads 31 us), 16 rows 19 us, 64 rows 35 us; 64 tokens through 222 of 256
-// experts of 7168 x 2048 290 us (6.0 TB/s; 497 us).  A single copying wave issues too slowly for a CU's
-// share of the stream: with two, 1 row over 2048 x 7168 takes 6.8 us instead of 8.4, with 64 rows four
-// take 33 us where one takes 46.
+// E8M0 rows of a number of scales that is not a multiple of 4 do not start on dwords, so they cannot be copied as such:
+// the multiplying waves read those bytes from memory where they use them (18432 x 7200 against 7168, time a byte:
+// bf16 x 1.2 to 1.5 times, fp16 x with scales of 32 twice; experts 1.3 to 3.3 times).
+//
+// Measured (18432 x 7168, fp32 scales of 128; the same weights in each call, which the last-level cache holds): 1 row
+// 15.1 us (4.6 TB/s of weights and scales; fragment-shaped register loads 31 us), 16 rows 17.5 us, 64 rows 32 us.  Weights
+// from memory: 17.6, 21.8 and 35.0 us.  64 tokens through 222 of 256 experts of 7168 x 2048 276 to 282 us (6.2 TB/s; 497 us).
+// A single copying wave issues too slowly for a CU's share of the stream: with two, 1 row over 2048 x 7168 takes
+// 6.8 us instead of 8.4, with 64 rows four take 33 us where one takes 46.
 #include "skinny.h"
 
 #include <type_traits>
@@ -128,7 +133,8 @@ struct Format {
   // fp16 products with E8M0 scales of 32, four in a block: the conversion takes a scale relative to the
   // block's largest and the fold that one.  Relative scales of at least 2^-13 keep e2m1's values (from 0.5 on)
   // normal in fp16, so exact; a wave that holds a smaller one folds that block's groups one by one.  Four folds
-  // a block for all instead: 64 rows, 18432 x 7168, 106 us (42 now); 16 rows 25.0 (22.0); 1 row 22.9 (18.9).
+  // a block for all instead: 64 rows, 18432 x 7168, 106 us (38.7 now); 16 rows 25.0 (20.4); 1 row 22.9 (17.3).
+  // Groups of 64 could do the same with their two scales; they fold twice a block (35.5, 20.4 and 17.5 us).
   static constexpr bool kRelative = W == kFp4E8M0 && F16 && GROUP == 32;
   static constexpr int kSpread = 13;
   static constexpr int kPerScale = kFold && !kRelative ? GROUP / 32 : 4;  // MFMAs that share a fold

@@ -540,7 +540,7 @@ def gemm_fp4_groupscale_workspace(M, N, K):
 
 def gemm_fp4_groupscale(x, q, scale, group=128, c=None, workspace=None):
     """x bf16 or fp16 [M, K] times 4-bit weights q [N, K/2] with scales [N, ceil(K/group)] (fp32, or
-    uint8 for E8M0), transposed: [M, N] in the type of x.
+    uint8 for E8M0), transposed: [M, N] in the type of x.  E8M0 rows of a multiple of 4 scales are fastest.
 
     workspace: None allocates what gemm_fp4_groupscale_workspace asks for (nothing up to 16
     rows); False runs without (K not split); or a device uint8 tensor.
@@ -640,8 +640,8 @@ class _GroupedLinear(torch.autograd.Function):
 
 
 def grouped_linear(x, w, offsets):
-    """grouped_gemm with gradients for x and w.  Every row of x must lie in a segment
-    (offsets[0] == 0 and offsets[E] == R): rows in none have no defined output or gradient."""
+    """grouped_gemm with gradients for x and w, in their type (grouped_gemm_wgrad also gives fp32).  Every row of
+    x must lie in a segment (offsets[0] == 0 and offsets[E] == R): rows in none have no defined output or gradient."""
     return _GroupedLinear.apply(x, w, offsets)
 
 
