@@ -10,7 +10,10 @@ from .moe355 import (  # noqa: F401
     Moe355Error,
     fp4_dequant_groups,
     fp4_quant_groups,
+    fp8_quant_128x128,
     fp8_quant_1x128,
+    fp8_quant_ragged,
+    fp8_ragged_blocks,
     gemm_fp4_groupscale,
     gemm_fp4_groupscale_workspace,
     gemm_fp8_blockscale,
@@ -21,16 +24,24 @@ from .moe355 import (  # noqa: F401
     grouped_gemm,
     grouped_gemm_dgrad,
     grouped_gemm_fp4,
+    grouped_gemm_fp8,
+    grouped_gemm_fp8_wgrad,
     grouped_gemm_wgrad,
     grouped_linear,
+    grouped_linear_fp8,
     grouped_topk,
     lib,
     moe_block_m,
+    moe_combine,
+    moe_combine_grad,
+    moe_dispatch,
     moe_down_combine,
     moe_down_combine_workspace,
     moe_fp8_blockscale_fused,
     moe_fp8_blockscale_fused_workspace,
     moe_fp8_blockscale_g1u1,
+    moe_group,
+    moe_group_workspace,
     moe_sort,
     moe_sort_sizes,
     shuffle_weight_128x128,

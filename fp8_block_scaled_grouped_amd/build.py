@@ -19,11 +19,12 @@ TRACE_LIB = os.path.join(PKG, "libmoe355_trace.so")
 # standalone probe programs (tuning/<name>.hip -> <package>/<name>)
 PROBES = ["lds_fill_probe", "kstep_probe", "e4m3_cvt_check"]
 SOURCES = ["gemm.hip", "gemm_big.hip", "dense_small.hip", "topk.hip", "sort.hip", "quant.hip", "shuffle.hip",
-           "fp4.hip", "skinny.hip", "ragged_gemm.hip", "status.cpp"]
+           "fp4.hip", "skinny.hip", "ragged_gemm.hip", "dispatch.hip", "fp8_pack.hip", "fp8_ragged.hip", "status.cpp"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 # per-source extra flags: MFMA results in VGPRs so the fp32 fold reads them directly
-EXTRA = {"gemm.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"], "gemm_big.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+EXTRA = {"gemm.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"], "gemm_big.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+         "fp8_ragged.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
 HIP_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",

@@ -52,6 +52,17 @@ _SIGNATURES = {
     "grouped_gemm": ([_vp, _i32, _i64, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _i64, _vp], _i32),
     "grouped_gemm_dgrad": ([_vp, _i32, _i64, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _i64, _vp], _i32),
     "grouped_gemm_wgrad": ([_vp, _i32, _i64, _vp, _i64, _vp, _i32, _i32, _i32, _i32, _vp, _i32, _vp], _i32),
+    "moe_group_workspace": ([_i32, _i32, _i32, _PSZ], _i32),
+    "moe_group": ([_vp, _i64, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _sz, _vp], _i32),
+    "moe_dispatch": ([_vp, _i32, _i64, _i32, _i32, _i32, _vp, _i32, _vp, _i64, _vp], _i32),
+    "moe_combine": ([_vp, _i32, _i64, _i32, _i32, _i32, _vp, _i32, _vp, _i64, _vp, _i64, _vp], _i32),
+    "moe_combine_grad": ([_vp, _i64, _vp, _i64, _i32, _i32, _i32, _i32, _vp, _i32, _vp, _i64, _vp, _i64, _vp, _vp], _i32),
+    "fp8_ragged_blocks": ([_i32, _i32, _P64], _i32),
+    "fp8_quant_ragged": ([_vp, _i32, _i64, _vp, _i32, _i32, _i32, _vp, _i64, _vp, _i64, _i64, _vp, _vp, _vp], _i32),
+    "fp8_quant_128x128": ([_vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _i32, _vp], _i32),
+    "grouped_gemm_fp8": ([_vp, _vp, _i64, _i64, _i64, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _vp, _i64, _i32, _vp],
+                         _i32),
+    "grouped_gemm_fp8_wgrad": ([_vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _i32, _vp], _i32),
 }
 # the pre-shuffled-weight variants take the same arguments as their plain calls
 for _name in ("gemm_fp8_blockscale", "moe_fp8_blockscale_g1u1", "moe_down_combine"):
@@ -643,6 +654,313 @@ def grouped_linear(x, w, offsets):
     """grouped_gemm with gradients for x and w, in their type (grouped_gemm_wgrad also gives fp32).  Every row of
     x must lie in a segment (offsets[0] == 0 and offsets[E] == R): rows in none have no defined output or gradient."""
     return _GroupedLinear.apply(x, w, offsets)
+
+
+# ----------------------------------------------------------------- tokens to rows and back
+_ELEM = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2, torch.uint8: 3}
+
+
+def _elem(t, name, most=2):
+    """The library's number of a device tensor's element type, among the first `most + 1`."""
+    n = _ELEM.get(t.dtype, 9)
+    if n > most or not t.is_cuda:
+        raise ValueError("%s must be a bf16, fp16 or fp32%s GPU tensor, got %s on %s"
+                         % (name, " or uint8" if most == 3 else "", t.dtype, t.device))
+    return n
+
+
+def _here(*tensors):
+    """The kernels are queued on the current GPU's stream: every tensor has to be on that GPU."""
+    dev = torch._C._cuda_getDevice()
+    for t in tensors:
+        if t is not None and t.device.index != dev:
+            raise ValueError("tensors must be on the current GPU (cuda:%d), got one on %s" % (dev, t.device))
+
+
+def _pairs(row_of_pair):
+    if row_of_pair.dim() != 2 or row_of_pair.shape[1] < 1:
+        raise ValueError("row_of_pair must be [T, topk]")
+    _need(row_of_pair, row_of_pair.shape, torch.int32, "row_of_pair")
+    return row_of_pair.shape
+
+
+def _grad_wanted(*tensors):
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+
+
+def moe_group_workspace(T, topk, E):
+    """Bytes of workspace that moe_group needs (host-only)."""
+    b = ctypes.c_size_t()
+    _check(lib().moe_group_workspace(T, topk, E, ctypes.byref(b)))
+    return b.value
+
+
+def moe_group(topk_ids, E, out=None, workspace=None):
+    """Token-expert pairs in expert order: (offsets [E+1], row_of_pair [T, topk], pair_of_row [T*topk]), all int32.
+
+    topk_ids int32 [T, topk] (rows may be strided).  The pairs of expert e get rows [offsets[e], offsets[e+1])
+    in ascending order; pairs whose id is outside [0, E) get row -1, and rows at or past offsets[E] pair -1.
+    """
+    _dev(topk_ids, torch.int32, "topk_ids")
+    ld = _ld(topk_ids, "topk_ids")
+    T, k = topk_ids.shape
+    if out is None:
+        out = (topk_ids.new_empty(E + 1), topk_ids.new_empty((T, k)), topk_ids.new_empty(T * k))
+    offsets, row_of_pair, pair_of_row = out
+    for t, shape, name in ((offsets, (E + 1,), "offsets"), (row_of_pair, (T, k), "row_of_pair"), (pair_of_row, (T * k,), "pair_of_row")):
+        _need(t, shape, torch.int32, name)
+    if workspace is None and T * k > 4096:
+        workspace = topk_ids.new_empty(moe_group_workspace(T, k, E), dtype=torch.uint8)
+    _here(topk_ids, offsets, row_of_pair, pair_of_row, workspace)
+    ws, wsn = (None, 0) if workspace is None else (_ptr(_dev(workspace, torch.uint8, "workspace")), workspace.numel())
+    _check(lib().moe_group(_ptr(topk_ids), ld, T, k, E, _ptr(offsets), _ptr(row_of_pair), _ptr(pair_of_row), ws, wsn, _stream()))
+    return offsets, row_of_pair, pair_of_row
+
+
+class _Dispatch(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, row_of_pair):
+        ctx.save_for_backward(row_of_pair)
+        return moe_dispatch(x, row_of_pair)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, drows):
+        return moe_combine(drows.contiguous(), *ctx.saved_tensors), None
+
+
+def moe_dispatch(x, row_of_pair, rows=None):
+    """Tokens x [T, H] (bf16, fp16, fp32 or uint8) to the rows of their pairs: rows[row_of_pair[t, j]] = x[t].
+
+    rows [T*topk, H], or any number of rows when given; rows that no pair has are left as they are.  Differentiable for x
+    (moe_combine without weights) when rows is not given.
+    """
+    if rows is None and _grad_wanted(x):
+        return _Dispatch.apply(x, row_of_pair)
+    dt = _elem(x, "x", 3)
+    T, k = _pairs(row_of_pair)
+    if x.dim() != 2 or x.shape[0] != T:
+        raise ValueError("x must be [T, H] with the tokens of row_of_pair")
+    H = x.shape[1]
+    if rows is None:
+        rows = x.new_empty((T * k, H))
+    elif rows.dim() != 2 or rows.shape[1] != H:
+        raise ValueError("rows must be [R, %d]" % H)
+    _dev(rows, x.dtype, "rows")
+    _here(x, row_of_pair, rows)
+    _check(lib().moe_dispatch(_ptr(x), dt, _ld(x, "x"), T, H, k, _ptr(row_of_pair), rows.shape[0], _ptr(rows), _ld(rows, "rows"),
+                              _stream()))
+    return rows
+
+
+class _Combine(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, rows, row_of_pair, weights):
+        ctx.save_for_backward(rows, row_of_pair, weights)
+        return moe_combine(rows, row_of_pair, weights)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dout):
+        rows, row_of_pair, weights = ctx.saved_tensors
+        drows, dw = moe_combine_grad(dout.contiguous(), rows, row_of_pair, weights, want=ctx.needs_input_grad[0::2])
+        return drows, None, dw
+
+
+def _routing_weights(weights, T, k):
+    _dev(weights, torch.float32, "weights")
+    if weights.shape != (T, k):
+        raise ValueError("weights must be %s, got %s" % ((T, k), tuple(weights.shape)))
+    return _ld(weights, "weights")
+
+
+def moe_combine(rows, row_of_pair, weights=None, out=None):
+    """Rows [R, H] (bf16, fp16 or fp32) back to tokens: out[t] = sum over j of weights[t, j] * rows[row_of_pair[t, j]],
+    [T, H] in the type of rows; fp32 sums over ascending j.  weights fp32 [T, topk], None for ones.
+
+    Differentiable for rows and weights when weights are given and out is not.
+    """
+    if out is None and weights is not None and _grad_wanted(rows, weights):
+        return _Combine.apply(rows, row_of_pair, weights)
+    dt = _elem(rows, "rows")
+    T, k = _pairs(row_of_pair)
+    if rows.dim() != 2:
+        raise ValueError("rows must be [R, H]")
+    R, H = rows.shape
+    ld_w = 0 if weights is None else _routing_weights(weights, T, k)
+    out = _out(out, (T, H), rows.dtype, rows, "out")
+    _here(rows, row_of_pair, weights, out)
+    _check(lib().moe_combine(_ptr(rows), dt, _ld(rows, "rows"), T, H, k, _ptr(row_of_pair), R, _ptr(weights), ld_w, _ptr(out),
+                             _ld(out, "out"), _stream()))
+    return out
+
+
+def moe_combine_grad(dout, rows, row_of_pair, weights, drows=None, dweights=None, want=(True, True)):
+    """Gradients of moe_combine: dout [T, H] -> (drows [R, H] in the type of rows, dweights fp32 [T, topk]).
+
+    Rows that no pair has are left as they are (of a new drows: undefined); a pair without a row has a dweights of 0.
+    want: which of the two to compute (None for the other).
+    """
+    dt = _elem(rows, "rows")
+    T, k = _pairs(row_of_pair)
+    if rows.dim() != 2:
+        raise ValueError("rows must be [R, H]")
+    R, H = rows.shape
+    _dev(dout, rows.dtype, "dout")
+    if dout.shape != (T, H):
+        raise ValueError("dout must be %s, got %s" % ((T, H), tuple(dout.shape)))
+    ld_w = _routing_weights(weights, T, k)
+    drows = _out(drows, (R, H), rows.dtype, rows, "drows") if want[0] else None
+    dweights = _need(_out(dweights, (T, k), torch.float32, weights, "dweights"), (T, k), torch.float32, "dweights") if want[1] else None
+    _here(dout, rows, row_of_pair, weights, drows, dweights)
+    _check(lib().moe_combine_grad(_ptr(dout), _ld(dout, "dout"), _ptr(rows), _ld(rows, "rows"), dt, T, H, k, _ptr(row_of_pair), R,
+                                  _ptr(weights), ld_w, _ptr(drows), 0 if drows is None else _ld(drows, "drows"), _ptr(dweights),
+                                  _stream()))
+    return drows, dweights
+
+
+# ----------------------------------------------------------------- FP8 products over ragged groups
+def fp8_ragged_blocks(R, E):
+    """Number of 128-row blocks that fp8_quant_ragged's transposed output has room for (host-only)."""
+    n = ctypes.c_int64()
+    _check(lib().fp8_ragged_blocks(R, E, ctypes.byref(n)))
+    return n.value
+
+
+def fp8_quant_ragged(x, offsets=None, rows=True, columns=True):
+    """Quantise rows x [R, K] (bf16 or fp16) ordered by expert to e4m3 with power-of-two scales (E8M0, uint8).
+
+    rows: (q uint8 [R, K], scale uint8 [R, ceil(K/128)]), one scale for each 1 x 128.  columns (needs offsets): (qt uint8
+    [blocks, K, 128], tscale uint8 [blocks, K]), one scale for each 128 rows of an expert x 1 column, as
+    grouped_gemm_fp8_wgrad takes them.  Returns (q, scale, qt, tscale) with None for what is not asked for.  Rows in no
+    segment are neither read nor written.  scale is stored by K blocks (its transpose is contiguous).
+    """
+    f16 = _half(x, "x")
+    ld = _ld(x, "x")
+    R, K = x.shape
+    columns = columns and offsets is not None
+    E = 0
+    if offsets is not None:
+        E = offsets.shape[0] - 1
+        _need(offsets, (E + 1,), torch.int32, "offsets")
+    q = scale = qt = tscale = None
+    if rows:
+        q = x.new_empty((R, K), dtype=torch.uint8)
+        scale = x.new_empty((_nblk(K), R), dtype=torch.uint8).t()
+    if columns:
+        blocks = fp8_ragged_blocks(R, E)
+        qt, tscale = x.new_empty((blocks, K, 128), dtype=torch.uint8), x.new_empty((blocks, K), dtype=torch.uint8)
+    if q is None and qt is None:
+        raise ValueError("neither rows nor columns asked for (columns need offsets)")
+    _here(x, offsets)
+    _check(lib().fp8_quant_ragged(_ptr(x), f16, ld, _ptr(offsets), R, E, K, _ptr(q), K, _ptr(scale), 1, R, _ptr(qt), _ptr(tscale),
+                                  _stream()))
+    return q, scale, qt, tscale
+
+
+def fp8_quant_128x128(w, scale_format="e8m0", transposed=False):
+    """Quantise weights w [E, N, K] (bf16 or fp16) to e4m3 with one scale for each 128 x 128: (q, scale), and with
+    transposed=True also (qt [E, K, N], tscale) of the same values.
+
+    scale_format "e8m0": uint8 power-of-two scales; "fp32": fp32 scales amax/448.
+    """
+    f16 = _half(w, "w")
+    if scale_format not in ("fp32", "e8m0"):
+        raise ValueError("scale_format must be 'fp32' or 'e8m0'")
+    if w.dim() != 3 or not w.is_contiguous():
+        raise ValueError("w must be a contiguous [E, N, K] tensor")
+    E, N, K = w.shape
+    sdt = torch.uint8 if scale_format == "e8m0" else torch.float32
+    q, scale = w.new_empty((E, N, K), dtype=torch.uint8), w.new_empty((E, _nblk(N), _nblk(K)), dtype=sdt)
+    qt = tscale = None
+    if transposed:
+        qt, tscale = w.new_empty((E, K, N), dtype=torch.uint8), w.new_empty((E, _nblk(K), _nblk(N)), dtype=sdt)
+    _here(w)
+    _check(lib().fp8_quant_128x128(_ptr(w), f16, E, N, K, _ptr(q), _ptr(scale), _ptr(qt), _ptr(tscale), int(scale_format == "e8m0"),
+                                   _stream()))
+    return (q, scale, qt, tscale) if transposed else (q, scale)
+
+
+def grouped_gemm_fp8(x8, x_scale, w8, w_scale, offsets, y=None, out_dtype=torch.bfloat16, scale_layout="row"):
+    """Rows x8 [R, K] (e4m3 codes, uint8) ordered by expert (offsets int32 [E+1] on the device) times the experts' weights
+    w8 [E, N, K], transposed: [R, N] in bf16 or fp16 (out_dtype, or the type of y when given).
+
+    Scales: x_scale [R, ceil(K/128)] of any strides ([ceil(K/128), R] with scale_layout "kblock") and w_scale [E, ceil(N/128),
+    ceil(K/128)], both fp32 (fp8_quant_1x128, checkpoints) or both uint8 for E8M0 (fp8_quant_ragged, fp8_quant_128x128).
+    Not differentiable (grouped_linear_fp8 is).
+    """
+    _dev(x8, torch.uint8, "x8")
+    ld = _ld(x8, "x8")
+    R, K = x8.shape
+    E, N, _ = w8.shape
+    _need(w8, (E, N, K), torch.uint8, "w8")
+    e8m0 = _fp4_scale(w_scale, (E, _nblk(N), _nblk(K)), "w_scale")
+    _dev(x_scale, w_scale.dtype, "x_scale")
+    if scale_layout == "kblock":
+        x_scale = x_scale.t()
+    elif scale_layout != "row":
+        raise ValueError("scale_layout must be 'row' or 'kblock'")
+    if x_scale.shape != (R, _nblk(K)):
+        raise ValueError("x_scale must have shape %s, got %s" % ((R, _nblk(K)), tuple(x_scale.shape)))
+    _need(offsets, (E + 1,), torch.int32, "offsets")
+    y = _out(y, (R, N), out_dtype if y is None else y.dtype, x8, "y")
+    _here(x8, x_scale, w8, w_scale, offsets, y)
+    _check(lib().grouped_gemm_fp8(_ptr(x8), _ptr(x_scale), ld, x_scale.stride(0), x_scale.stride(1), _ptr(w8), _ptr(w_scale), e8m0,
+                                  _ptr(offsets), R, E, N, K, _ptr(y), _ld(y, "y"), _half(y, "y"), _stream()))
+    return y
+
+
+def grouped_gemm_fp8_wgrad(dyt, dyt_scale, xt, xt_scale, offsets, R, dw=None, out_dtype=torch.float32):
+    """Gradient of grouped_gemm_fp8 for w from the transposed codes of dy and x (fp8_quant_ragged's qt and tscale of R
+    rows): [E, N, K] in fp32, bf16 or fp16 (out_dtype, or the type of dw when given).  Experts without rows get zeros."""
+    E = offsets.shape[0] - 1
+    _need(offsets, (E + 1,), torch.int32, "offsets")
+    blocks, N, K = fp8_ragged_blocks(R, E), dyt.shape[1], xt.shape[1]
+    for t, shape, name in ((dyt, (blocks, N, 128), "dyt"), (dyt_scale, (blocks, N), "dyt_scale"), (xt, (blocks, K, 128), "xt"),
+                           (xt_scale, (blocks, K), "xt_scale")):
+        _need(t, shape, torch.uint8, name)
+    dt = out_dtype if dw is None else dw.dtype
+    dw = _need(_out(dw, (E, N, K), dt, dyt, "dw"), (E, N, K), dt, "dw")
+    _here(dyt, dyt_scale, xt, xt_scale, offsets, dw)
+    _check(lib().grouped_gemm_fp8_wgrad(_ptr(dyt), _ptr(dyt_scale), _ptr(xt), _ptr(xt_scale), _ptr(offsets), R, E, N, K, _ptr(dw),
+                                        _elem(dw, "dw"), _stream()))
+    return dw
+
+
+class _GroupedLinearFp8(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, offsets):
+        need_x, need_w = ctx.needs_input_grad[:2]
+        q, scale, qt, tscale = fp8_quant_ragged(x, offsets, columns=need_w)
+        packed = fp8_quant_128x128(w, transposed=need_x)
+        ctx.save_for_backward(offsets, qt, tscale, *packed[2:])
+        ctx.w_dtype, ctx.x_dtype = w.dtype, x.dtype
+        return grouped_gemm_fp8(q, scale, *packed[:2], offsets, out_dtype=x.dtype)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        offsets, qt, tscale, *wt = ctx.saved_tensors
+        need_x, need_w = ctx.needs_input_grad[:2]
+        dy = dy.contiguous()
+        if dy.data_ptr() % 16:  # a view into a larger gradient may start anywhere
+            dy = dy.clone()
+        q, scale, dyt, dyts = fp8_quant_ragged(dy, offsets, rows=need_x, columns=need_w)
+        dx = grouped_gemm_fp8(q, scale, *wt, offsets, out_dtype=ctx.x_dtype) if need_x else None
+        dw = grouped_gemm_fp8_wgrad(dyt, dyts, qt, tscale, offsets, dy.shape[0], out_dtype=ctx.w_dtype) if need_w else None
+        return dx, dw, None
+
+
+def grouped_linear_fp8(x, w, offsets):
+    """grouped_linear in FP8: x [R, K] and w [E, N, K] (bf16 or fp16, the same type) are quantised to e4m3 with a power-of-two
+    scale for each block (x 1 x 128, w 128 x 128) and multiplied, and so are the gradients: dx from dy in 1 x 128 and
+    the same w, dw from dy and x in blocks of 128 rows x 1.  What the backward pass keeps is x and w in 8 bits.
+
+    N and K multiples of 16.  Every row of x must lie in a segment: rows in none have no defined output or gradient.
+    """
+    if x.dtype != w.dtype:
+        raise ValueError("x and w must have the same type, got %s and %s" % (x.dtype, w.dtype))
+    return _GroupedLinearFp8.apply(x, w, offsets)
 
 
 # ----------------------------------------------------------------- the layer

@@ -432,6 +432,99 @@ int grouped_gemm_wgrad(const uint16_t* dy, int fp16, int64_t ld_dy, const uint16
                        const int32_t* offsets, int R, int E, int N, int K, void* dw, int out_fp32,
                        hipStream_t stream);
 
+/* Element types of the calls below. */
+#define MOE355_BF16 0
+#define MOE355_F16 1
+#define MOE355_F32 2
+#define MOE355_U8 3
+
+/* Host-only workspace query for moe_group (no GPU access). */
+int moe_group_workspace(int T, int topk, int E, size_t* bytes);
+
+/*
+ * Token-expert pairs in expert order without padding: the segments that the ragged products take.  Pair
+ * p = t*topk + j belongs to expert topk_ids[t, j]; the pairs of expert e, in ascending p, get the rows
+ * [offsets[e], offsets[e+1]).
+ *   offsets      int32 [E+1] out, offsets[0] = 0 and offsets[E] = the number of pairs with a row
+ *   row_of_pair  int32 [T*topk] out: the pair's row, -1 for an id outside [0, E) (an expert held elsewhere)
+ *   pair_of_row  int32 [T*topk] out or NULL: the row's pair, -1 for rows at or past offsets[E]
+ * topk_ids [T, topk], row stride ld_topk.  workspace: moe_group_workspace bytes (contents need no
+ * initialisation), 0 up to 4096 pairs.  1 <= E <= 1024 and T*topk < 2^31, else MOE355_EUNSUPPORTED.
+ */
+int moe_group(const int32_t* topk_ids, int64_t ld_topk, int T, int topk, int E, int32_t* offsets,
+              int32_t* row_of_pair, int32_t* pair_of_row, void* workspace, size_t workspace_bytes,
+              hipStream_t stream);
+
+/*
+ * Tokens to rows and back, with row_of_pair [T, topk] as moe_group writes it.  A pair whose row is not in
+ * [0, R) is left out, and rows that no pair has are neither read nor written.
+ *   moe_dispatch      rows[row_of_pair[t, j], :] = x[t, :]
+ *   moe_combine       out[t, :] = round(sum over ascending j of weights[t, j] * rows[row_of_pair[t, j], :])
+ *                     (fp32 sums; weights NULL: ones, which is the gradient of moe_dispatch)
+ *   moe_combine_grad  drows[row_of_pair[t, j], :] = round(weights[t, j] * dout[t, :])
+ *                     dweights[t, j] = sum_h dout[t, h] * rows[row_of_pair[t, j], h]   (fp32; 0 without a row)
+ * x, out, dout [T, H], rows, drows [R, H]: MOE355_BF16, _F16 or _F32 (moe_dispatch also _U8), row strides ld_*.
+ * weights fp32 [T, topk], row stride ld_weights; dweights fp32 [T, topk].  drows or dweights may be NULL.
+ * No two pairs share a row.  Any H; rows that start on 16 bytes and hold a multiple of 16 are faster.
+ * Every sum has a fixed order.
+ */
+int moe_dispatch(const void* x, int dtype, int64_t ld_x, int T, int H, int topk, const int32_t* row_of_pair,
+                 int R, void* rows, int64_t ld_rows, hipStream_t stream);
+int moe_combine(const void* rows, int dtype, int64_t ld_rows, int T, int H, int topk, const int32_t* row_of_pair,
+                int R, const float* weights, int64_t ld_weights, void* out, int64_t ld_out, hipStream_t stream);
+int moe_combine_grad(const void* dout, int64_t ld_dout, const void* rows, int64_t ld_rows, int dtype, int T,
+                     int H, int topk, const int32_t* row_of_pair, int R, const float* weights, int64_t ld_weights,
+                     void* drows, int64_t ld_drows, float* dweights, hipStream_t stream);
+
+/*
+ * FP8 operands of the ragged expert products.  E8M0 scales: one byte c that stands for 2^(c - 127), 255 for
+ * NaN; a block's scale is the smallest power of two that keeps it in +-448 (exponent kept in [-127, 127], 1 for
+ * a block of zeros) and q = e4m3(x / scale), nearest even.  A block that holds a NaN or an infinity gets scale 255.
+ *
+ * fp8_quant_ragged: x [R, K] (bf16 bits, fp16 bits when fp16 is 1; row stride ld_x), rows ordered by expert.
+ *   q, scale    along rows: e4m3 [R, K] (row stride ld_q), one scale for each 1 x 128, (m, kb) at
+ *               scale[m*sstride_m + kb*sstride_kb]; the last group of a row may be shorter
+ *   qt, tscale  along columns, for a product over the rows: one scale for each 128 rows x 1 column, the rows
+ *               counted from the expert's first.  qt e4m3 [blocks, K, 128], tscale [blocks, K], where expert e's
+ *               blocks start at offsets[e]/128 + e and blocks = fp8_ragged_blocks(R, E) (some stay unused
+ *               and are not written); rows past the segment's end are zeros.
+ * Either pair may be NULL.  With offsets NULL the rows are one segment (q and scale only; E is not read).
+ * K % 8 == 0, E < 65536 else MOE355_EUNSUPPORTED; x, q, qt 16-byte aligned, ld_x and ld_q multiples of 8.
+ *
+ * fp8_quant_128x128: weights w [E, N, K] -> q the same shape and scale [E, ceil(N/128), ceil(K/128)], one for each
+ * 128 x 128: E8M0, or fp32 (e8m0 = 0; amax/448 and the quotients as in fp8_quant_1x128, NaN for a block that is not
+ * finite).  qt and tscale (NULL for none) hold the same codes and scales transposed, [E, K, N] and
+ * [E, ceil(K/128), ceil(N/128)].  K % 8 == 0 and with qt N % 16 == 0, else MOE355_EUNSUPPORTED.
+ */
+int fp8_ragged_blocks(int R, int E, int64_t* blocks);
+int fp8_quant_ragged(const uint16_t* x, int fp16, int64_t ld_x, const int32_t* offsets, int R, int E, int K,
+                     uint8_t* q, int64_t ld_q, uint8_t* scale, int64_t sstride_m, int64_t sstride_kb,
+                     uint8_t* qt, uint8_t* tscale, hipStream_t stream);
+int fp8_quant_128x128(const uint16_t* w, int fp16, int E, int N, int K, uint8_t* q, void* scale,
+                      uint8_t* qt, void* tscale, int e8m0, hipStream_t stream);
+
+/*
+ * FP8 expert products over ragged groups (offsets as above), fp32 sums:
+ *   grouped_gemm_fp8        y[r, n] = round(sum_kb x_scale(r,kb) * w_scale[e, n/128, kb] *
+ *                                           sum_{k in kb} x8[r, k] * w8[e, n, k])
+ *   grouped_gemm_fp8_wgrad  dw[e, n, k] = round(sum over e's blocks b of dyt_scale[b, n] * xt_scale[b, k] *
+ *                                               sum_{i < 128} dyt[b, n, i] * xt[b, k, i])
+ * x8 e4m3 [R, K], row stride ld_x; x_scale(r,kb) = x_scale[r*sstride_m + kb*sstride_kb]; w8 e4m3 [E, N, K] and w_scale
+ * [E, ceil(N/128), ceil(K/128)]: both scales fp32, or E8M0 bytes when e8m0 is 1.  y [R, N] bf16 bits, or fp16 bits when
+ * fp16 is 1.  The gradient for x is the same call on dy's rows and the transposed weights.
+ * dyt [blocks, N, 128], xt [blocks, K, 128] and their scales as fp8_quant_ragged writes them; dw [E, N, K] of type
+ * out (MOE355_BF16, _F16 or _F32); an expert without rows gets zeros.
+ * grouped_gemm_fp8: N % 8 == 0, K % 16 == 0, ld_x and N up to 4194304; wgrad: N % 8 == 0, K % 8 == 0, both up to
+ * 4194304; E < 65536; else MOE355_EUNSUPPORTED.  Pointers (scales excepted) 16-byte aligned, ld_x a multiple of 16 and
+ * ld_y of 8, else MOE355_EMISALIGNED.
+ */
+int grouped_gemm_fp8(const uint8_t* x8, const void* x_scale, int64_t ld_x, int64_t sstride_m, int64_t sstride_kb,
+                     const uint8_t* w8, const void* w_scale, int e8m0, const int32_t* offsets, int R, int E,
+                     int N, int K, uint16_t* y, int64_t ld_y, int fp16, hipStream_t stream);
+int grouped_gemm_fp8_wgrad(const uint8_t* dyt, const uint8_t* dyt_scale, const uint8_t* xt,
+                           const uint8_t* xt_scale, const int32_t* offsets, int R, int E, int N, int K, void* dw,
+                           int out, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

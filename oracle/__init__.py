@@ -26,6 +26,8 @@ moe      gate/up + SiLU*up + requantisation, down projection + combine,
 layout   the pre-shuffled 128x128-tile weight layout (a byte permutation)
 fp4      4-bit (OCP e2m1) weights with group scales
 ragged   products grouped by expert over ragged row segments, and their gradients
+dispatch tokens to the rows of their experts and back, with gradients
+fp8_ragged  FP8 operands of the ragged products (power-of-two scales along rows, columns and blocks)
 pool     runs independent pieces (experts, blocks of rows) on host threads
 """
-from . import fp8, pool, quant, routing, sort, gemm, moe, layout, fp4, ragged  # noqa: F401
+from . import fp8, pool, quant, routing, sort, gemm, moe, layout, fp4, ragged, dispatch, fp8_ragged  # noqa: F401
