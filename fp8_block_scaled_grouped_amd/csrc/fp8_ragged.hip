@@ -12,14 +12,18 @@
 //
 // Ragged edges cost no branch in the loop: every LDS-DMA goes through a buffer descriptor that ends with
 // the operand's last valid byte, so rows past it arrive as zeros, and lanes whose chunk lies past the row's
-// width are sent past the end.
+// width are sent past the end; stores past the segment go past the end of one as well.
+//
+// What bounds it: 64 KB of operands into LDS for the 16.8 MFLOP of a 256 x 256 step next to the 192 KB of fragments that its waves read
+// back.  65536 rows over 32 experts of 4096 x 7168: 1.48 ms (2600 TFLOP/s) with power-of-two scales, 1.65 (2330) with fp32
+// ones, the gradient for w 1.67; a library product of 8192^3 without block scales runs at 2960 to 3000.  Without the DMAs a step's MFMAs
+// and reads alone took 1.20 ms, without the MFMAs 1.49.
 #include <type_traits>
 
 #include "device_common.h"
 #include "frag16.h"
 #include "gemm_engine.h"
 #include "host_common.h"
-#include "ragged_tile.h"
 
 namespace moe355 {
 namespace {
@@ -38,28 +42,14 @@ struct Fp8Args {
   int f16;                 // 16-bit outputs: fp16 or bf16
 };
 
-// One operand of a step: ROWS rows of 128 codes, chunk c of row r in slot c ^ (r & 7), filled by NW waves with NI DMAs each.
-template <int ROWS, int NW>
-struct Operand8 {
-  static constexpr int kBytes = ROWS * 128;
-  static constexpr int NI = kBytes / 1024 / NW;
-  static_assert(NI * NW * 1024 == kBytes, "whole DMAs");
-  uint32_t off[NI];
-  int kc;  // this lane's k within the step
+// LDS-DMA of a dword a lane, as dma16_buf.
+__device__ __forceinline__ void dma4_buf(u32x4 rsrc, uint32_t off, uint32_t m0) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds" ::"v"(off), "s"(rsrc), "s"(m0)
+               : "memory");
+}
 
-  __device__ __forceinline__ void init(int w, int lane, int64_t ld) {
-    const int c = (lane & 7) ^ (lane >> 3);
-    kc = 16 * c;
-#pragma unroll
-    for (int i = 0; i < NI; ++i) off[i] = (uint32_t)((8 * (w * NI + i) + (lane >> 3)) * ld + kc);
-  }
-  __device__ __forceinline__ void dma(int i, u32x4 rsrc, uint32_t lds, int w, uint32_t past) const {
-    dma16_buf(rsrc, off[i] | past, lds + (w * NI + i) * 1024);
-  }
-  __device__ __forceinline__ uint32_t past(int krem) const { return kc >= krem ? kPastEnd : 0u; }
-};
-
-// Fragment f (16 rows) of a staged operand: lane l row l % 16, chunks l / 16 and l / 16 + 4.  `at` is the lane's place in fragment 0.
+// Fragment f (16 rows) of a staged operand, chunk c of whose row r stands in slot c ^ (r & 7): lane l has row l % 16, chunks
+// l / 16 and l / 16 + 4.  `at` is the lane's place in fragment 0.
 __device__ __forceinline__ uint32_t frag_at(int row0, int lane) {
   return (row0 + (lane & 15)) * 128 + (((lane >> 4) ^ (lane & 7)) << 4);
 }
@@ -69,254 +59,460 @@ __device__ __forceinline__ v8i read_frag(uint32_t lds, uint32_t at, int f) {
   const u32x4 hi = *reinterpret_cast<p>(lds + (at ^ 64) + f * 2048);
   return v8i{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
 }
-
-// Lane l's values of 16 T rows (row l % (16 T)) -> for each tile of 16 rows that of row l % 16, in every lane.
-template <int T>
-__device__ __forceinline__ void spread(uint32_t v, uint32_t (&s)[T]) {
-  static_assert(T == 1 || T == 2 || T == 4, "tiles of a wave");
-  if constexpr (T == 1) {
-    s[0] = v;
-  } else if constexpr (T == 2) {
-    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-    s[0] = r[0];
-    s[1] = r[1];
-  } else {
-    const auto h = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-    const auto lo = __builtin_amdgcn_permlane16_swap(h[0], h[0], false, false);
-    const auto hi = __builtin_amdgcn_permlane16_swap(h[1], h[1], false, false);
-    s[0] = lo[0];
-    s[1] = lo[1];
-    s[2] = hi[0];
-    s[3] = hi[1];
-  }
+__device__ __forceinline__ uint32_t read_u32(uint32_t lds) {
+  return *reinterpret_cast<__attribute__((address_space(3))) uint32_t*>(lds);
 }
 
-// D = A B scaled by 2^(sa - 127) 2^(sb - 127) for each row of A and column of B, + C
+// D = A B scaled by 2^(sa - 127) 2^(sb - 127) for each row of A and column of B, + C; of sa and sb the low bytes count
 __device__ __forceinline__ v4f mfma_scaled(const v8i& a, const v8i& b, const v4f& c, uint32_t sa, uint32_t sb) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, (int)sa, 0, (int)sb);
 }
 
+// A workgroup's tiles: what its stream of operands needs of each, by lanes side by side before the first one.
+constexpr int kMaxTiles = 64;  // of a workgroup
+constexpr int kTab = 512;      // experts, or groups of `per` experts, that are found by their number of row tiles
+
+struct alignas(8) Tile {
+  int64_t a, b, sa, sb;              // first bytes of the operands and of their scales
+  int64_t row0;                      // first row of c
+  int lena, lenb, lensa, lensb;      // bytes from there to the end of the tile's first step (fwd: of its rows)
+  int steps, mrows, n0;
+};
+
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform64(int64_t v) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)((uint64_t)v >> 32));
+  return (int64_t)((uint64_t)hi << 32 | lo);
+}
+
+// Row tiles of expert e.
+__device__ __forceinline__ int row_tiles(const int32_t* offsets, int R, int e, int BM) {
+  int lo, hi;
+  segment(offsets, R, e, lo, hi);
+  return (hi - lo + BM - 1) / BM;
+}
+
+// Row tiles are numbered one expert after the other: tab[i] becomes the number of the first of expert i * per, INT_MAX past the last
+// expert.  By one wave; returns the number of row tiles to all lanes.  No number passes `most`, whatever the offsets hold.
+template <int BM>
+__device__ __forceinline__ int fill_table(const int32_t* offsets, int R, int E, int per, int most, int* tab, int lane) {
+  uint32_t first[kTab / 64], mine = 0;
+#pragma unroll
+  for (int i = 0; i < kTab / 64; ++i) {
+    first[i] = mine;
+    const int64_t e0 = (int64_t)(lane * (kTab / 64) + i) * per;
+    for (int64_t e = e0; e < e0 + per && e < E; ++e) mine = min(mine + row_tiles(offsets, R, (int)e, BM), (uint32_t)most);
+  }
+  uint32_t before = __shfl_up(mine, 1, 64);  // tiles of the lanes before this one
+  if (lane == 0) before = 0;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const uint32_t v = __shfl_up(before, o, 64);
+    if (lane >= o) before = min(before + v, (uint32_t)most);
+  }
+#pragma unroll
+  for (int i = 0; i < kTab / 64; ++i) {
+    const bool in = (int64_t)(lane * (kTab / 64) + i) * per < E;
+    tab[lane * (kTab / 64) + i] = in ? (int)min(before + first[i], (uint32_t)most) : 0x7fffffff;
+  }
+  return (int)__shfl(min(before + mine, (uint32_t)most), 63, 64);
+}
+
+// Expert of row tile q, and the number of its first one.
+template <int BM>
+__device__ __forceinline__ int find_expert(const int32_t* offsets, int R, int E, int per, const int* tab, int q, int& first) {
+  int at = 0;
+#pragma unroll
+  for (int o = kTab / 2; o > 0; o >>= 1)
+    if (tab[at + o] <= q) at += o;
+  int e = at * per;
+  first = tab[at];
+  for (; e + 1 < E; ++e) {  // past tab[at]'s first expert where an entry stands for several
+    const int m = row_tiles(offsets, R, e, BM);
+    if (q < first + m) break;
+    first += m;
+  }
+  return e;
+}
+
+// Two sums rounded to 16 bits (hardware conversions, nearest even).
+template <bool F16>
+__device__ __forceinline__ uint32_t pack16(float a, float b) {
+  if constexpr (F16) return __builtin_bit_cast(uint32_t, f16x2{(_Float16)a, (_Float16)b});
+  else return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b});
+}
+
+// Stores a wave's sums and clears them: lane l holds of tile (i, j) the row 16 i + l % 16 and the four columns from 16 j + 4 (l / 16).
+// c: the wave's first row and column; rows and cols are left from there on (fewer than none: nothing is stored).  Stores past them
+// go past the end of a buffer descriptor, so there is no branch.
+// 16-bit: pairs of column tiles change lanes so that a lane holds 8 columns, 16 bytes; fp32: so that a store covers 8 rows of
+// 128 bytes rather than 16 of 64.
+template <bool F16, bool OUT32, int TM, int TN>
+__device__ __forceinline__ void store_sums(v4f (&acc)[TM][TN], void* c, int64_t ldc, int rows, int cols, int lane) {
+  constexpr int kSize = OUT32 ? 4 : 2;
+  const int r = min(rows, 16 * TM);
+  const uint32_t ld = (uint32_t)ldc * kSize;
+  const int bytes = rows > 0 && cols > 0 ? (int)((uint32_t)(r - 1) * ld) + min(cols, 16 * TN) * kSize : 0;
+  const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(c, 0, bytes, 0x00020000);
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+#pragma unroll
+    for (int j = 0; j < TN; j += 2) {
+      if constexpr (OUT32) {
+        const bool up = lane & 8;
+        u32x4 first, second;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t p = __float_as_uint(acc[i][j][k]), q = __float_as_uint(acc[i][j + 1][k]);
+          const uint32_t y = __builtin_amdgcn_update_dpp(0, up ? p : q, 0x128, 0xf, 0xf, true);  // from lane l ^ 8
+          first[k] = up ? y : p;
+          second[k] = up ? q : y;
+        }
+        const int n = 4 * (lane >> 4) + 16 * (j + (up ? 1 : 0));
+        const uint32_t at = n < cols ? (16 * i + (lane & 7)) * ld + n * kSize : kPastEnd;
+        __builtin_amdgcn_raw_buffer_store_b128(first, rsrc, at, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(second, rsrc, at + 8 * ld, 0, 0);
+      } else {
+        const v4f &x = acc[i][j], &y = acc[i][j + 1];
+        const auto lo = __builtin_amdgcn_permlane16_swap(pack16<F16>(x[0], x[1]), pack16<F16>(y[0], y[1]), false, false);
+        const auto hi = __builtin_amdgcn_permlane16_swap(pack16<F16>(x[2], x[3]), pack16<F16>(y[2], y[3]), false, false);
+        // lanes of groups 0 and 2 hold columns 0 .. 7 and 8 .. 15 of tile j, those of 1 and 3 of tile j + 1
+        const int n = 16 * (j + ((lane >> 4) & 1)) + 8 * (lane >> 5);
+        const uint32_t at = n < cols ? (16 * i + (lane & 15)) * ld + n * kSize : kPastEnd;
+        __builtin_amdgcn_raw_buffer_store_b128(u32x4{lo[0], hi[0], lo[1], hi[1]}, rsrc, at, 0, 0);
+      }
+      acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+      acc[i][j + 1] = v4f{0.f, 0.f, 0.f, 0.f};
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+}
+
 // E8: power-of-two scales (bytes), else fp32 ones.  Waves stand WM x WN, each with TM x TN tiles of 16 x 16.
-// A step reads the wave's TM fragments of A once, ahead of it, and streams the TN fragments of B kAhead ahead.  In the
-// middle of step s a wait and a barrier publish the operands of step s + 1; at that point A(s) (in registers since step s - 1)
-// and B(s - 1) are done with, so their slots take step s + 2: two slots of A and three of B.
+//
+// The steps of all tiles of a workgroup are one stream: while one tile's last steps are multiplied and its sums are
+// stored, the operands of the next are on their way.  A step's rows j = 0 .. TN - 1 multiply fragment j of B with the TM fragments of A.
+// A(s) is read ahead, during step s - 1; B's fragments are read two rows ahead.  Two barriers a step:
+//   row 1     A(s) is in everyone's registers and B(s - 1) is done with: A(s + 2) and its scales follow into A(s)'s slot
+//   row TN/2  A(s + 1), B(s + 1) and their scales have landed (the DMAs of A(s + 2) may be under way) and the first half of B(s)'s
+//             fragments is done with: B(s + 2) follows, its halves in the slots of the second half of B(s - 1) and the first of B(s)
+// So LDS holds two slots of A and five halves of B, and DMAs go out in every part of a step.  Measured on 65536 rows over 32 experts of
+// 4096 x 7168, E8M0 (fp32 scales; gradient for w): one barrier a step, all DMAs in its second half and scales loaded into registers
+// 1.80 ms (1.87; 2.15); so 1.48 (1.65; 1.67), most of the last from one tile's start under another's end: with 8 steps a tile (16384 rows
+// over 32 experts of 4096 x 2048) 0.229 ms against 0.320.
 template <int OP, bool E8, bool OUT32, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_ragged_kernel(Fp8Args g) {
   constexpr int NW = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
-  constexpr int kAhead = 1, kHold = 2;  // fragments of B ahead, and held
-  using OA = Operand8<BM, NW>;
-  using OB = Operand8<BN, NW>;
-  __shared__ __align__(16) uint8_t smem[2 * OA::kBytes + 3 * OB::kBytes];
+  constexpr int kAhead = TM * TN >= 32 ? 1 : 2, kHold = 2 * kAhead, kHalf = TN / 2;  // fragments of B ahead, and held
+  constexpr int kABytes = BM * 128, kHBytes = BN * 64;  // a slot of A, a half of B
+  constexpr int NA = kABytes / 1024 / NW, NH = kHBytes / 1024 / NW;  // DMAs of a wave
+  constexpr int kWin = (BM + BN) / 64;                   // 64 scales each: BM of A, then BN of B
+  constexpr int kScales = 4 * (BM + BN);                 // scales of a step, a dword each
+  static_assert(NA * NW * 1024 == kABytes && NH * NW * 1024 == kHBytes && NW % kWin == 0 && TN >= 4 && TN % 4 == 0, "whole DMAs");
+  static_assert(kHalf - 1 >= 1 && NA + 1 < 64, "A's DMAs go out in rows 1 .. TN/2 - 1");
+  __shared__ __align__(16) uint8_t smem[2 * kABytes + 5 * kHBytes + 3 * kScales];
+  __shared__ Tile tiles[kMaxTiles];
+  __shared__ int count_sh;
   const int tid = threadIdx.x, lane = tid & 63;
-  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = (w / WN) * (BM / WM), wn = (w % WN) * (BN / WN);
+  const int w = uniform(tid >> 6);
+  const int wm = (w / WN) * (BM / WM), wi = w % WN;
 
   const int ndim = OP == kFp8Fwd ? g.N : g.K, ntiles = (ndim + BN - 1) / BN;
-  int e, mt, nt, lo, hi;
-  if constexpr (OP == kFp8Wgrad) {
-    const int mtiles = (g.N + BM - 1) / BM;
-    const int64_t total = (int64_t)g.E * mtiles * ntiles, chunk = (total + 7) / 8;
-    const int64_t t = (int64_t)(blockIdx.x & 7) * chunk + (blockIdx.x >> 3);
-    if ((blockIdx.x >> 3) >= chunk || t >= total) return;
-    e = (int)(t / ((int64_t)mtiles * ntiles));
-    const int in = (int)(t - (int64_t)e * mtiles * ntiles), band = 8 * ntiles, b0 = in / band * 8;
-    const int height = min(8, mtiles - b0);
-    mt = b0 + in % band % height;
-    nt = in % band / height;
-  } else {
-    if (!place<BM>(g.offsets, g.R, g.E, ntiles, reinterpret_cast<int*>(smem), e, mt, nt)) return;
-    __syncthreads();  // the place has been read: the DMAs may overwrite it
+  const int KB = (g.K + 127) / 128;
+  constexpr int kEsz = E8 ? 1 : 4;
+  if (w == 0) {
+    const int mtiles = (g.N + BM - 1) / BM, per = (g.E + kTab - 1) / kTab;
+    int* tab = reinterpret_cast<int*>(smem);
+    const int total = OP == kFp8Fwd ? fill_table<BM>(g.offsets, g.R, g.E, per, g.R / BM + min(g.E, g.R), tab, lane) * ntiles : g.E * mtiles * ntiles;
+    // each XCD (workgroups go to the eight in turn) takes a run of the tiles, and its workgroups the next one in turn
+    const int chunk = (total + 7) / 8, stride = gridDim.x >> 3;
+    const int first = (int)(blockIdx.x & 7) * chunk + (int)(blockIdx.x >> 3), end = min(total, ((int)(blockIdx.x & 7) + 1) * chunk);
+    if (lane == 0) count_sh = first < end ? min(kMaxTiles, (end - first + stride - 1) / stride) : 0;
+    const int64_t t = first + (int64_t)lane * stride;
+    if (t < end) {
+      const int q = (int)t / ntiles;
+      int e, base, m, lo, hi;
+      if constexpr (OP == kFp8Fwd) {
+        e = find_expert<BM>(g.offsets, g.R, g.E, per, tab, q, base);
+        m = row_tiles(g.offsets, g.R, e, BM);
+      } else {
+        e = q / mtiles;
+        base = e * mtiles;
+        m = mtiles;
+      }
+      segment(g.offsets, g.R, e, lo, hi);
+      // inside an expert the tiles advance in bands of 8 row tiles: those that an XCD works on at a time share few panels
+      const int rest = (int)t - base * ntiles, band = 8 * ntiles, b0 = max(0, rest) / band * 8, in = max(0, rest) % band;
+      const int height = max(1, min(8, m - b0)), mt = b0 + in % height;
+      const bool known = rest >= 0 && mt < m;  // always, unless the offsets decrease
+      const int m0 = known ? mt * BM : 0, n0 = in / height * BN;
+      const int left = !known ? 0 : OP == kFp8Fwd ? hi - lo - m0 : g.N - m0, mrows = min(BM, left), nrows = min(BN, ndim - n0);
+      const int64_t block0 = lo / 128 + e;  // wgrad: the segment's first block
+      Tile x;
+      x.steps = !known || n0 >= ndim ? 0 : OP == kFp8Fwd ? KB : (hi - lo + 127) / 128;
+      x.mrows = left;
+      x.n0 = n0;
+      if constexpr (OP == kFp8Fwd) {
+        x.row0 = lo + m0;
+        x.a = (int64_t)(lo + m0) * g.lda;
+        x.b = ((int64_t)e * g.N + n0) * g.K;
+        x.lena = (int)((mrows - 1) * g.lda + g.K);
+        x.lenb = (int)((nrows - 1) * (int64_t)g.K + g.K);
+        x.sa = (int64_t)(lo + m0) * g.ssm * kEsz;
+        x.sb = ((int64_t)e * ((g.N + 127) / 128) + n0 / 128) * KB * kEsz;
+        x.lensa = (int)(((mrows - 1) * g.ssm + 1) * kEsz);
+        x.lensb = ((nrows - 1) / 128 * KB + 1) * kEsz;
+      } else {
+        x.row0 = (int64_t)e * g.N + m0;
+        x.a = (block0 * g.N + m0) * 128;
+        x.b = (block0 * g.K + n0) * 128;
+        x.lena = mrows * 128;
+        x.lenb = nrows * 128;
+        x.sa = block0 * g.N + m0;
+        x.sb = block0 * g.K + n0;
+        x.lensa = mrows;
+        x.lensb = nrows;
+      }
+      tiles[lane] = x;
+    }
   }
-  e = __builtin_amdgcn_readfirstlane(e);
-  mt = __builtin_amdgcn_readfirstlane(mt);
-  nt = __builtin_amdgcn_readfirstlane(nt);
-  segment(g.offsets, g.R, e, lo, hi);
-  lo = __builtin_amdgcn_readfirstlane(lo);
-  hi = __builtin_amdgcn_readfirstlane(hi);
+  __syncthreads();
+  const int count = uniform(count_sh);
+  if (count == 0) return;
 
-  const int m0 = mt * BM, n0 = nt * BN;
-  const int kdim = OP == kFp8Fwd ? g.K : (hi - lo + 127) / 128 * 128;
-  const int steps = (kdim + 127) / 128;
-  const int mrows = OP == kFp8Wgrad ? g.N - m0 : hi - lo - m0;  // m left from the tile's first on
-  const int nrows = ndim - n0;
-  const int64_t block0 = lo / 128 + e;  // wgrad: the segment's first block
-
-  // first byte of the tile's operands, what a step adds, and bytes from there to the end
+  // ---- the stream of operands: all uniform but the lanes' offsets, which hold for every tile
   const int64_t lda = OP == kFp8Fwd ? g.lda : 128, ldb = OP == kFp8Fwd ? g.K : 128;
-  const uint8_t* pa = OP == kFp8Fwd ? g.a + (int64_t)(lo + m0) * lda : g.a + (block0 * g.N + m0) * 128;
-  const uint8_t* pb = OP == kFp8Fwd ? g.b + ((int64_t)e * g.N + n0) * ldb : g.b + (block0 * g.K + n0) * 128;
   const int64_t stepa = OP == kFp8Fwd ? 128 : (int64_t)g.N * 128, stepb = OP == kFp8Fwd ? 128 : (int64_t)g.K * 128;
-  int64_t lena = (min(mrows, BM) - 1) * lda + (OP == kFp8Fwd ? kdim : 128);
-  int64_t lenb = (min(nrows, BN) - 1) * ldb + (OP == kFp8Fwd ? kdim : 128);
+  const int kc = 16 * ((lane & 7) ^ (lane >> 3));  // this lane's k within a step
+  const uint32_t offa = (uint32_t)((lane >> 3) * lda + kc), offb = (uint32_t)((lane >> 3) * ldb + kc);
+  // DMA i of A moves rows 8 (w NA + i) .., of half h of B 8 rows of the first or second halves of all column waves' fragments
+  auto rowa = [&](int i) { return (uint32_t)(8 * (w * NA + i) * lda); };
+  auto rowb = [&](int h, int i) {
+    constexpr int kPart = BN / WN / 2;
+    const int r = 8 * (w * NH + i);
+    return (uint32_t)((r / kPart * (2 * kPart) + h * kPart + r % kPart) * ldb);
+  };
+  // scales: window w % kWin, one lane a row of A or column of B
+  const int64_t stepsa = (OP == kFp8Fwd ? g.sskb : g.N) * kEsz, stepsb = OP == kFp8Fwd ? kEsz : g.K;  // from one step to the next
+  const int win = w % kWin;
+  const bool of_a = win < BM / 64;  // uniform
+  const int srow = 64 * (of_a ? win : win - BM / 64) + lane;
+  const uint32_t soff = (uint32_t)((of_a ? srow * (OP == kFp8Fwd ? g.ssm : 1) : OP == kFp8Fwd ? srow / 128 * (int64_t)KB : srow) * kEsz);
+  int ft = -1, fs = 0, fsteps = 0;  // tile and step of the next operands
+  const uint8_t *pa = nullptr, *pb = nullptr, *ps = nullptr;
+  int lena = 0, lenb = 0, lens = 0;
+  // E8: where a step's bytes start in their dwords, of A's scales and of B's (this step's, the next one's, the one fetched)
+  uint32_t lowa = 0, lowb = 0, rema[3], remb[3];
+  // to the next tile that has steps; past the last one nothing is fetched
+  auto seek = [&]() __attribute__((always_inline)) {
+    fs = 0;
+    do {
+      ++ft;
+    } while (ft < count && (fsteps = uniform(tiles[ft].steps)) == 0);
+    if (ft < count) {
+      const Tile* x = tiles + ft;
+      pa = g.a + uniform64(x->a);
+      pb = g.b + uniform64(x->b);
+      const uint8_t* psa = static_cast<const uint8_t*>(g.sa) + uniform64(x->sa);
+      const uint8_t* psb = static_cast<const uint8_t*>(g.sb) + uniform64(x->sb);
+      lowa = (uint32_t)(uintptr_t)psa;
+      lowb = (uint32_t)(uintptr_t)psb;
+      ps = of_a ? psa : psb;
+      lena = uniform(x->lena);
+      lenb = uniform(x->lenb);
+      lens = uniform(of_a ? x->lensa : x->lensb);
+    } else {
+      lena = lenb = lens = -(1 << 30);
+      fsteps = 0x7fffffff;
+    }
+  };
+  u32x4 da, db, ds;
+  uint32_t past = 0, srem = 0;
+  auto next_a = [&]() __attribute__((always_inline)) {  // and the scales
+    da = dma_buffer(pa, lena);
+    past = OP == kFp8Fwd && kc >= g.K - fs * 128 ? kPastEnd : 0u;
+    pa += stepa;
+    if (OP == kFp8Fwd) lena -= 128;
+    // scales of a byte are fetched with the dword around them
+    srem = E8 ? (uint32_t)(uintptr_t)ps & 3u : 0u;
+    ds = dma_buffer(ps - srem, (lens + (int)srem + 3) & ~3);
+    ps += of_a ? stepsa : stepsb;
+    rema[2] = lowa;
+    remb[2] = lowb;
+    lowa += (uint32_t)stepsa;
+    lowb += (uint32_t)stepsb;
+  };
+  auto next_b = [&]() __attribute__((always_inline)) {
+    db = dma_buffer(pb, lenb);
+    pb += stepb;
+    if (OP == kFp8Fwd) lenb -= 128;
+    ++fs;
+  };
+  const uint32_t lds0 = lds_addr(smem), ldss = lds0 + 2 * kABytes + 5 * kHBytes;
+  auto dma_a = [&](int i, uint32_t slot) { dma16_buf(da, (offa | past) + rowa(i), slot + (w * NA + i) * 1024); };
+  auto dma_b = [&](int h, int i, uint32_t slot) { dma16_buf(db, (offb | past) + rowb(h, i), slot + (w * NH + i) * 1024); };
+  auto dma_s = [&](uint32_t slot) { dma4_buf(ds, E8 ? (soff + srem) & ~3u : soff, slot + win * 256); };
 
-  OA oa;
-  OB ob;
-  oa.init(w, lane, lda);
-  ob.init(w, lane, ldb);
-  const uint32_t ata = frag_at(wm, lane), atb = frag_at(wn, lane);
-  const uint32_t lds0 = lds_addr(smem);
-
+  // ---- the products
+  const uint32_t ata = frag_at(wm, lane), atb = frag_at(wi * (BN / WN / 2), lane);
+  const uint32_t atsa = 4 * (wm + (lane & 15)), atsb = 4 * (BM + wi * (BN / WN) + (OP == kFp8Wgrad ? (lane & 15) : 0));
+  const uint32_t mod_a = (lane & 15) * (OP == kFp8Fwd ? (uint32_t)g.ssm : 1u);
+  const uint32_t mod_b = OP == kFp8Fwd ? (uint32_t)(wi * (BN / WN) / 128 * KB) : lane & 15;
   v4f acc[TM][TN];
 #pragma unroll
   for (int i = 0; i < TM; ++i)
 #pragma unroll
     for (int j = 0; j < TN; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
 
-  // scales of a step: this lane's row of A (its last valid one past the end) and, wgrad, its columns of B
-  constexpr int kSB = OP == kFp8Wgrad ? (TN + 3) / 4 : 1;
-  const int arow = min(wm + lane % (16 * TM), mrows - 1);
-  const int64_t sa0 = OP == kFp8Fwd ? (int64_t)(lo + m0 + arow) * g.ssm : block0 * g.N + m0 + arow;
-  const int64_t sastep = OP == kFp8Fwd ? g.sskb : g.N;
-  int64_t sb0[kSB];
-  if constexpr (OP == kFp8Wgrad) {
+  uint32_t hb[5], sl[2] = {lds0, lds0 + kABytes};  // halves of B and slots of A: this step's, the next one's, ..
 #pragma unroll
-    for (int q = 0; q < kSB; ++q) sb0[q] = block0 * g.K + n0 + min(wn + 64 * q + lane % (16 * min(TN, 4)), nrows - 1);
-  } else {
-    const int KB = (g.K + 127) / 128;
-    sb0[0] = ((int64_t)e * ((g.N + 127) / 128) + (n0 + wn < g.N ? n0 + wn : n0) / 128) * KB;
-  }
-  auto scale_at = [&](const void* p, int64_t i) {
-    if constexpr (E8) return (uint32_t) static_cast<const uint8_t*>(p)[i];
-    else return static_cast<const uint32_t*>(p)[i];
-  };
-  auto scale_a = [&](int s) { return scale_at(g.sa, sa0 + min(s, steps - 1) * sastep); };
-  auto scale_b = [&](int s, int q) {
-    const int t = min(s, steps - 1);
-    return scale_at(g.sb, OP == kFp8Wgrad ? sb0[q] + (int64_t)t * g.K : sb0[q] + t);
-  };
-
-  u32x4 da, db;
-  uint32_t pasta, pastb;
-  int ka = 0, kb = 0;  // first k of the next A and B
-  auto next_a = [&] {
-    da = dma_buffer(pa, ka < kdim ? lena : 0);
-    pasta = OP == kFp8Fwd ? oa.past(kdim - ka) : 0;
-    pa += stepa;
-    if (OP == kFp8Fwd) lena -= 128;
-    ka += 128;
-  };
-  auto next_b = [&] {
-    db = dma_buffer(pb, kb < kdim ? lenb : 0);
-    pastb = OP == kFp8Fwd ? ob.past(kdim - kb) : 0;
-    pb += stepb;
-    if (OP == kFp8Fwd) lenb -= 128;
-    kb += 128;
-  };
-
-  if (steps > 0) {
-    uint32_t rawa[2] = {scale_a(0), scale_a(1)}, rawb[2][kSB];
+  for (int i = 0; i < 5; ++i) hb[i] = lds0 + 2 * kABytes + i * kHBytes;
+  uint32_t sc = ldss, sn = ldss + kScales, sf = ldss + 2 * kScales;  // scales of this step and of the next two
+  vm_wait<0>();
 #pragma unroll
-    for (int q = 0; q < kSB; ++q) {
-      rawb[0][q] = scale_b(0, q);
-      rawb[1][q] = scale_b(1, q);
-    }
-    uint32_t b0 = lds0 + 2 * OA::kBytes, b1 = b0 + OB::kBytes, b2 = b1 + OB::kBytes;
-    vm_wait<0>();
+  for (int s = 0; s < 2; ++s) {
+    if (fs == fsteps) seek();
     next_a();
 #pragma unroll
-    for (int i = 0; i < OA::NI; ++i) oa.dma(i, da, lds0, w, pasta);
+    for (int i = 0; i < NA; ++i) dma_a(i, sl[s]);
+    dma_s(s ? sn : sc);
+    rema[s] = rema[2];
+    remb[s] = remb[2];
     next_b();
 #pragma unroll
-    for (int i = 0; i < OB::NI; ++i) ob.dma(i, db, b0, w, pastb);
-    next_a();
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int i = 0; i < OA::NI; ++i) oa.dma(i, da, lds0 + OA::kBytes, w, pasta);
-    next_b();
+      for (int i = 0; i < NH; ++i) dma_b(h, i, hb[2 * s + h]);
+  }
+  vm_wait<NA + 1 + 2 * NH>();
+  barrier_only();
+  v8i ra[2][TM], rb[kHold];
+  uint32_t rawa[TM], rawb[kHold];  // scales of A's fragments (this step's, then the next one's) and of B's held ones
 #pragma unroll
-    for (int i = 0; i < OB::NI; ++i) ob.dma(i, db, b1, w, pastb);
-    vm_wait<OA::NI + OB::NI>();
-    barrier_only();
-    v8i ra[2][TM], rb[kHold];
+  for (int i = 0; i < TM; ++i) {
+    ra[0][i] = read_frag(lds0, ata, i);
+    rawa[i] = read_u32(sc + atsa + 64 * i);
+  }
 #pragma unroll
-    for (int i = 0; i < TM; ++i) ra[0][i] = read_frag(lds0, ata, i);
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) rb[j] = read_frag(b0, atb, j);
+  for (int j = 0; j < kAhead; ++j) {
+    rb[j] = read_frag(hb[0], atb, j);
+    rawb[j] = read_u32(sc + atsb + (OP == kFp8Wgrad ? 64 * j : 0));
+  }
 
-    auto step = [&](int s, auto par_c) {
-      constexpr int PAR = decltype(par_c)::value;
-      const uint32_t acur = lds0 + PAR * OA::kBytes, anext = lds0 + (PAR ^ 1) * OA::kBytes;
-      uint32_t sa[TM], sb[kSB][TN < 4 ? TN : 4];
-      spread<TM>(rawa[0], sa);
-      if constexpr (OP == kFp8Wgrad) {
+  auto step = [&](auto par_c) __attribute__((always_inline)) {
+    constexpr int PAR = decltype(par_c)::value;
+    // a byte's place in its dword is the same for all of a lane's rows (16 apart), and for its columns
+    const uint32_t sha = E8 ? 8 * ((mod_a + rema[0]) & 3) : 0, shb = E8 ? 8 * ((mod_b + remb[0]) & 3) : 0;
+    uint32_t sa[TM];
+    float f[TM];
 #pragma unroll
-        for (int q = 0; q < kSB; ++q) spread<(TN < 4 ? TN : 4)>(rawb[0][q], sb[q]);
-      }
-      float f[TM];
-      if constexpr (!E8) {
-#pragma unroll
-        for (int i = 0; i < TM; ++i) f[i] = __uint_as_float(sa[i]) * __uint_as_float(rawb[0][0]);
-      }
-      const uint32_t sbu = rawb[0][0];
-      v4f t[3];
-      constexpr int kHalf = TN / 2;
-      constexpr int kDmas = (OA::NI + OB::NI + kHalf - 1) / kHalf, kReads = (TM + kHalf - 1) / kHalf;
-#pragma unroll
-      for (int j = 0; j < TN; ++j) {
-        if (j == kHalf) {
-          vm_wait<0>();    // this wave's share of step s + 1 has landed, and its scales
-          barrier_only();  // everyone's has, and nobody reads A(s) and B(s - 1) any more
-          rawa[0] = rawa[1];
-          rawa[1] = scale_a(s + 2);
-#pragma unroll
-          for (int q = 0; q < kSB; ++q) {
-            rawb[0][q] = rawb[1][q];
-            rawb[1][q] = scale_b(s + 2, q);
-          }
-          next_a();
-          next_b();
-        }
-        if (j + kAhead < TN) rb[(j + kAhead) % kHold] = read_frag(b0, atb, j + kAhead);
-        else rb[(j + kAhead) % kHold] = read_frag(b1, atb, j + kAhead - TN);
-        if (j >= kHalf) {
-#pragma unroll
-          for (int d = (j - kHalf) * kReads; d < (j - kHalf + 1) * kReads && d < TM; ++d) ra[PAR ^ 1][d] = read_frag(anext, ata, d);
-#pragma unroll
-          for (int d = (j - kHalf) * kDmas; d < (j - kHalf + 1) * kDmas; ++d) {
-            if (d < OA::NI) oa.dma(d, da, acur, w, pasta);
-            else if (d < OA::NI + OB::NI) ob.dma(d - OA::NI, db, b2, w, pastb);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < TM; ++i) {
-          if constexpr (E8) {
-            acc[i][j] = mfma_scaled(rb[j % kHold], ra[PAR][i], acc[i][j], OP == kFp8Wgrad ? sb[j / 4][j % 4] : sbu, sa[i]);
-          } else {
-            // the fold of the tile before the last follows each MFMA
-            const int q = j * TM + i;
-            t[q % 3] = mfma16x16x128_fp8(rb[j % kHold], ra[PAR][i], v4f{0.f, 0.f, 0.f, 0.f});
-            if (q >= 2) {
-              const int p = q - 2;
-              acc[p % TM][p / TM] += t[p % 3] * f[p % TM];
-            }
-          }
-          if constexpr (!E8) __builtin_amdgcn_sched_barrier(0);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      if constexpr (!E8) {
-#pragma unroll
-        for (int p = TM * TN - 2; p < TM * TN; ++p) acc[p % TM][p / TM] += t[p % 3] * f[p % TM];
-      }
-      const uint32_t was = b0;
-      b0 = b1;
-      b1 = b2;
-      b2 = was;
-    };
-    int s = 0;
-    for (; s + 1 < steps; s += 2) {
-      step(s, std::integral_constant<int, 0>{});
-      step(s + 1, std::integral_constant<int, 1>{});
+    for (int i = 0; i < TM; ++i) {
+      if constexpr (E8) sa[i] = rawa[i] >> sha;
+      else f[i] = __uint_as_float(rawa[i]) * __uint_as_float(rawb[0]);
     }
-    if (s < steps) step(s, std::integral_constant<int, 0>{});
-    vm_wait<0>();
+    const uint32_t sbu = rawb[0] >> shb;  // fwd: one for all of the wave's columns
+    v4f acc2[3];
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      if (j == 1) {
+        barrier_only();
+        next_a();
+      }
+      if (j == kHalf) {
+        vm_wait<NA + 1>();
+        barrier_only();
+        next_b();
+      }
+      const int ahead = j + kAhead;
+      rb[ahead % kHold] = read_frag(ahead < TN ? hb[ahead / kHalf] : hb[2], atb, ahead % kHalf);
+      if constexpr (OP == kFp8Wgrad) rawb[ahead % kHold] = read_u32((ahead < TN ? sc : sn) + atsb + 64 * (ahead % TN));
+      if (j >= 1 && j < kHalf) {
+        constexpr int kRow = (NA + 1 + kHalf - 2) / (kHalf - 1);
+#pragma unroll
+        for (int d = (j - 1) * kRow; d < j * kRow; ++d) {
+          if (d < NA) dma_a(d, sl[PAR]);
+          else if (d == NA) dma_s(sf);
+        }
+      }
+      if (j >= kHalf) {
+        constexpr int kRow = 2 * NH / kHalf, kReads = (TM + kHalf - 1) / kHalf;
+#pragma unroll
+        for (int d = (j - kHalf) * kRow; d < (j - kHalf + 1) * kRow; ++d) dma_b(d / NH, d % NH, hb[d < NH ? 4 : 0]);
+#pragma unroll
+        for (int d = (j - kHalf) * kReads; d < (j - kHalf + 1) * kReads && d < TM; ++d) {
+          ra[PAR ^ 1][d] = read_frag(sl[PAR ^ 1], ata, d);
+          rawa[d] = read_u32(sn + atsa + 64 * d);
+        }
+      }
+      if constexpr (OP == kFp8Fwd) {
+        if (j == TN - 1) rawb[0] = read_u32(sn + atsb);
+      }
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        if constexpr (E8) {
+          acc[i][j] = mfma_scaled(rb[j % kHold], ra[PAR][i], acc[i][j], OP == kFp8Wgrad ? rawb[j % kHold] >> shb : sbu, sa[i]);
+        } else {
+          // the fold of the tile before the last follows each MFMA
+          const int q = j * TM + i;
+          acc2[q % 3] = mfma16x16x128_fp8(rb[j % kHold], ra[PAR][i], v4f{0.f, 0.f, 0.f, 0.f});
+          if (q >= 2) {
+            const int p = q - 2;
+            acc[p % TM][p / TM] += acc2[p % 3] * f[p % TM];
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if constexpr (!E8) {
+#pragma unroll
+      for (int p = TM * TN - 2; p < TM * TN; ++p) acc[p % TM][p / TM] += acc2[p % 3] * f[p % TM];
+    }
+    // the sums stay in this step's block: products are not moved past the branches between steps
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) asm volatile("" : "+v"(acc[i][j]));
+    const uint32_t h0 = hb[0], h1 = hb[1], s0 = sc;
+    hb[0] = hb[2];
+    hb[1] = hb[3];
+    hb[2] = hb[4];
+    hb[3] = h0;
+    hb[4] = h1;
+    sc = sn;
+    sn = sf;
+    sf = s0;
+    rema[0] = rema[1];
+    rema[1] = rema[2];
+    remb[0] = remb[1];
+    remb[1] = remb[2];
+  };
+  for (int t = 0; t < count; ++t) {
+    int left = uniform(tiles[t].steps);
+    for (; left >= 2; left -= 2) {
+      if (fs == fsteps) seek();
+      step(std::integral_constant<int, 0>{});
+      if (fs == fsteps) seek();
+      step(std::integral_constant<int, 1>{});
+    }
+    if (left) {
+      if (fs == fsteps) seek();
+      step(std::integral_constant<int, 0>{});
+#pragma unroll
+      for (int i = 0; i < TM; ++i) ra[0][i] = ra[1][i];
+      const uint32_t was = sl[0];
+      sl[0] = sl[1];
+      sl[1] = was;
+    }
+    const int64_t row0 = uniform64(tiles[t].row0);
+    const int mrows = uniform(tiles[t].mrows), n0 = uniform(tiles[t].n0);
+    int l = lane;
+    asm volatile("" : "+v"(l));  // the stores' addresses are made here, not kept in registers through the steps
+    uint8_t* c = static_cast<uint8_t*>(g.c) + ((row0 + wm) * g.ldc + n0 + wi * (BN / WN)) * (OUT32 ? 4 : 2);
+    if (OUT32 || !g.f16) store_sums<false, OUT32>(acc, c, g.ldc, mrows - wm, ndim - n0 - wi * (BN / WN), l);
+    else store_sums<true, false>(acc, c, g.ldc, mrows - wm, ndim - n0 - wi * (BN / WN), l);
   }
-
-  const int64_t row0 = (OP == kFp8Wgrad ? (int64_t)e * g.N : (int64_t)lo) + m0;
-  if (OUT32 || !g.f16) {
-    store_tile<false, OUT32>(acc, g.c, g.ldc, row0, n0, mrows, nrows, wm, wn, lane);
-  } else {
-    store_tile<true, false>(acc, g.c, g.ldc, row0, n0, mrows, nrows, wm, wn, lane);
-  }
+  vm_wait<0>();
 }
 
 template <int OP, bool E8, bool OUT32, int BM, int BN, int WM, int WN>
@@ -325,8 +521,10 @@ int launch(const Fp8Args& g, hipStream_t stream) {
   const int64_t nt = ceil_div64(OP == kFp8Fwd ? g.N : g.K, BN);
   // an upper bound of the row tiles: the offsets are on the device
   const int64_t mt = OP == kFp8Wgrad ? (int64_t)g.E * ceil_div64(g.N, BM) : g.R / BM + (g.E < g.R ? g.E : g.R);
-  const int64_t grid = ceil_div64(mt * nt, 8) * 8;
-  MOE355_CHECK(grid * (64 * WM * WN) < (1ll << 32), MOE355_EUNSUPPORTED);  // threads of a launch
+  MOE355_CHECK(mt * nt < (1ll << 31), MOE355_EUNSUPPORTED);  // tiles are counted in 32 bits
+  // as many workgroups as the CUs hold at a time, or tiles; more where one would get more than kMaxTiles
+  const int64_t slots = 256 * (BM == 256 ? 1 : BM == 128 ? 2 : 3), need = ceil_div64(ceil_div64(mt * nt, 8), kMaxTiles) * 8;
+  const int64_t few = ceil_div64(mt * nt, 8) * 8 < slots ? ceil_div64(mt * nt, 8) * 8 : slots, grid = few > need ? few : need;
   hipLaunchKernelGGL(fn, dim3((unsigned)grid), dim3(64 * WM * WN), 0, stream, g);
   return launch_status();
 }
@@ -349,6 +547,7 @@ bool on4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 constexpr int64_t kMaxLd = 1 << 22;    // 256 rows' byte offsets stay below 2^31
 constexpr int kMaxDim = 1 << 22;
+constexpr int64_t kMaxSs = 1 << 21;    // and those of their scales
 
 }  // namespace
 }  // namespace moe355
@@ -361,7 +560,7 @@ extern "C" int grouped_gemm_fp8(const uint8_t* x8, const void* x_scale, int64_t 
   MOE355_CHECK((fp16 == 0 || fp16 == 1) && (e8m0 == 0 || e8m0 == 1) && R >= 0 && E >= 0 && N >= 0 && K >= 0 && ld_x >= K &&
                    ld_y >= N && sstride_m >= 0 && sstride_kb >= 0,
                MOE355_EINVAL);
-  MOE355_CHECK(N % 8 == 0 && K % 16 == 0 && N <= kMaxDim && E < 65536 && ld_x <= kMaxLd && ld_y <= (1ll << 40), MOE355_EUNSUPPORTED);
+  MOE355_CHECK(N % 8 == 0 && K % 16 == 0 && N <= kMaxDim && E < 65536 && ld_x <= kMaxLd && sstride_m <= kMaxSs && ld_y <= kMaxSs, MOE355_EUNSUPPORTED);
   if (R == 0 || E == 0 || N == 0) return MOE355_OK;
   MOE355_CHECK(offsets && y && (K == 0 || (x8 && w8 && x_scale && w_scale)), MOE355_EINVAL);
   MOE355_CHECK((K == 0 || (aligned16(x8) && ld_x % 16 == 0 && aligned16(w8))) && aligned16(y) && ld_y % 8 == 0 && on4(offsets) &&

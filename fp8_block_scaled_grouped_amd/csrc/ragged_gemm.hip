@@ -22,7 +22,6 @@
 #include "frag16.h"
 #include "gemm_engine.h"
 #include "host_common.h"
-#include "ragged_tile.h"
 #include "skinny.h"
 
 namespace moe355 {
@@ -101,6 +100,61 @@ struct Fragments {
   }
 };
 
+// Row tiles of expert e.
+__device__ __forceinline__ int row_tiles(const int32_t* offsets, int R, int e, int BM) {
+  int lo, hi;
+  segment(offsets, R, e, lo, hi);
+  return (hi - lo + BM - 1) / BM;
+}
+
+// A workgroup's place: expert, row tile and column tile.  Workgroups go to the 8 XCDs in turn, so
+// each XCD takes a contiguous run of the tiles, and inside an expert the tiles advance in
+// bands of 8 row tiles: the tiles that an XCD works on at a time share few panels.
+template <int BM>
+__device__ __forceinline__ bool place(const RaggedArgs& g, int ntiles, int* sh, int& e, int& mt, int& nt) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  if (tid < 64) {
+    const int per = (g.E + 63) / 64;
+    const int e0 = min(g.E, lane * per), e1 = min(g.E, e0 + per);
+    int mine = 0;
+    for (int i = e0; i < e1; ++i) mine += row_tiles(g.offsets, g.R, i, BM);
+    int upto = mine;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int v = __shfl_up(upto, o, 64);
+      if (lane >= o) upto += v;
+    }
+    const int rows = __shfl(upto, 63, 64);
+    const int64_t total = (int64_t)rows * ntiles, chunk = (total + 7) / 8;
+    const int64_t t = (int64_t)(blockIdx.x & 7) * chunk + (blockIdx.x >> 3);
+    if (lane == 0) sh[0] = -1;
+    if ((blockIdx.x >> 3) < chunk && t < total) {
+      // the lane whose experts hold tile t: tiles before this lane's experts are (upto - mine) * ntiles
+      const int64_t first = (int64_t)(upto - mine) * ntiles;
+      if (t >= first && t < (int64_t)upto * ntiles) {
+        int64_t rest = t - first;
+        for (int i = e0; i < e1; ++i) {
+          const int m = row_tiles(g.offsets, g.R, i, BM);
+          if (rest < (int64_t)m * ntiles) {
+            const int band = 8 * ntiles, b0 = (int)(rest / band) * 8, in = (int)(rest % band);
+            const int height = min(8, m - b0);
+            sh[0] = i;
+            sh[1] = b0 + in % height;
+            sh[2] = in / height;
+            break;
+          }
+          rest -= (int64_t)m * ntiles;
+        }
+      }
+    }
+  }
+  __syncthreads();
+  e = sh[0];
+  mt = sh[1];
+  nt = sh[2];
+  return e >= 0;
+}
+
 template <int OP, bool F16, bool OUT32, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN, 2) void ragged_gemm_kernel(RaggedArgs g) {
   constexpr bool AK = OP != kRaggedWgrad, BK = OP == kRaggedFwd;  // k along memory rows
@@ -126,7 +180,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void ragged_gemm_kernel(RaggedArgs
     mt = b0 + in % band % height;
     nt = in % band / height;
   } else {
-    if (!place<BM>(g.offsets, g.R, g.E, ntiles, reinterpret_cast<int*>(smem), e, mt, nt)) return;
+    if (!place<BM>(g, ntiles, reinterpret_cast<int*>(smem), e, mt, nt)) return;
     __syncthreads();  // the place has been read: the DMAs may overwrite it
   }
   e = __builtin_amdgcn_readfirstlane(e);
@@ -267,8 +321,54 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void ragged_gemm_kernel(RaggedArgs
     vm_wait<0>();
   }
 
+  // lane: row m of the tile, four adjacent n
+  const int nw = (w % WN) * (BN / WN) + 4 * (lane >> 4);
   const int64_t row0 = (OP == kRaggedWgrad ? (int64_t)e * g.N : (int64_t)lo) + m0;
-  store_tile<F16, OUT32>(acc, g.c, g.ldc, row0, n0, mrows, nrows, (w / WN) * (BM / WM), (w % WN) * (BN / WN), lane);
+  if constexpr (OUT32 && TN % 2 == 0) {
+    // pairs of column tiles exchange halves between lanes l and l ^ 8, so that a store covers 8 rows of
+    // 128 bytes rather than 16 rows of 64 (16384 rows over 32 experts of 4096 x 2048: 424 us against 437)
+    const bool up = lane & 8;
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+#pragma unroll
+      for (int j = 0; j < TN; j += 2) {
+        v4f first, second;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float x = up ? acc[i][j][k] : acc[i][j + 1][k];
+          const float y = __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x128, 0xf, 0xf, true));
+          first[k] = up ? y : acc[i][j][k];
+          second[k] = up ? acc[i][j + 1][k] : y;
+        }
+        const int n = nw + 16 * (j + (up ? 1 : 0));
+        if (n >= nrows) continue;
+        const int m = (w / WN) * (BM / WM) + 16 * i + (lane & 7);
+        float* out = reinterpret_cast<float*>(g.c) + (row0 + m) * g.ldc + n0 + n;
+        if (m < mrows) *reinterpret_cast<v4f*>(out) = first;
+        if (m + 8 < mrows) *reinterpret_cast<v4f*>(out + 8 * g.ldc) = second;
+      }
+    }
+  } else {
+    const int mw = (w / WN) * (BM / WM) + (lane & 15);
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      const int m = mw + 16 * i;
+      if (m >= mrows) continue;
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        const int n = nw + 16 * j;
+        if (n >= nrows) continue;  // nrows % 8 == 0: the four are all in or all out
+        const int64_t at = (row0 + m) * g.ldc + n0 + n;
+        if constexpr (OUT32) {
+          *reinterpret_cast<v4f*>(reinterpret_cast<float*>(g.c) + at) = acc[i][j];
+        } else {
+          const uint2 r{f32_to_out16(acc[i][j][0], F16) | (f32_to_out16(acc[i][j][1], F16) << 16),
+                        f32_to_out16(acc[i][j][2], F16) | (f32_to_out16(acc[i][j][3], F16) << 16)};
+          *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(g.c) + at) = r;
+        }
+      }
+    }
+  }
 }
 
 template <int OP, bool F16, bool OUT32, int BM, int BN, int WM, int WN>
