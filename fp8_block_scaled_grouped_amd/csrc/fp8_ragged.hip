@@ -18,6 +18,8 @@
 // back.  65536 rows over 32 experts of 4096 x 7168: 1.48 ms (2600 TFLOP/s) with power-of-two scales, 1.65 (2330) with fp32
 // ones, the gradient for w 1.67; a library product of 8192^3 without block scales runs at 2960 to 3000.  Without the DMAs a step's MFMAs
 // and reads alone took 1.20 ms, without the MFMAs 1.49.
+#include <math.h>
+
 #include <type_traits>
 
 #include "device_common.h"
@@ -206,9 +208,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_ragged_kernel(Fp8Args g) 
   constexpr int kAhead = TM * TN >= 32 ? 1 : 2, kHold = 2 * kAhead, kHalf = TN / 2;  // fragments of B ahead, and held
   constexpr int kABytes = BM * 128, kHBytes = BN * 64;  // a slot of A, a half of B
   constexpr int NA = kABytes / 1024 / NW, NH = kHBytes / 1024 / NW;  // DMAs of a wave
-  constexpr int kWin = (BM + BN) / 64;                   // 64 scales each: BM of A, then BN of B
-  constexpr int kScales = 4 * (BM + BN);                 // scales of a step, a dword each
-  static_assert(NA * NW * 1024 == kABytes && NH * NW * 1024 == kHBytes && NW % kWin == 0 && TN >= 4 && TN % 4 == 0, "whole DMAs");
+  constexpr int kWinA = (BM + 63) / 64, kWin = kWinA + BN / 64;  // windows of 64 scales: A's rows, then B's columns
+  constexpr int kScales = 256 * kWin;                    // scales of a step, a dword each
+  static_assert(NA * NW * 1024 == kABytes && NH * NW * 1024 == kHBytes && NW >= kWin && TN >= 4 && TN % 4 == 0, "whole DMAs");
   static_assert(kHalf - 1 >= 1 && NA + 1 < 64, "A's DMAs go out in rows 1 .. TN/2 - 1");
   __shared__ __align__(16) uint8_t smem[2 * kABytes + 5 * kHBytes + 3 * kScales];
   __shared__ Tile tiles[kMaxTiles];
@@ -295,8 +297,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_ragged_kernel(Fp8Args g) 
   // scales: window w % kWin, one lane a row of A or column of B
   const int64_t stepsa = (OP == kFp8Fwd ? g.sskb : g.N) * kEsz, stepsb = OP == kFp8Fwd ? kEsz : g.K;  // from one step to the next
   const int win = w % kWin;
-  const bool of_a = win < BM / 64;  // uniform
-  const int srow = 64 * (of_a ? win : win - BM / 64) + lane;
+  const bool of_a = win < kWinA;  // uniform
+  const int srow = 64 * (of_a ? win : win - kWinA) + lane;
   const uint32_t soff = (uint32_t)((of_a ? srow * (OP == kFp8Fwd ? g.ssm : 1) : OP == kFp8Fwd ? srow / 128 * (int64_t)KB : srow) * kEsz);
   int ft = -1, fs = 0, fsteps = 0;  // tile and step of the next operands
   const uint8_t *pa = nullptr, *pb = nullptr, *ps = nullptr;
@@ -355,7 +357,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_ragged_kernel(Fp8Args g) 
 
   // ---- the products
   const uint32_t ata = frag_at(wm, lane), atb = frag_at(wi * (BN / WN / 2), lane);
-  const uint32_t atsa = 4 * (wm + (lane & 15)), atsb = 4 * (BM + wi * (BN / WN) + (OP == kFp8Wgrad ? (lane & 15) : 0));
+  const uint32_t atsa = 4 * (wm + (lane & 15)), atsb = 4 * (64 * kWinA + wi * (BN / WN) + (OP == kFp8Wgrad ? (lane & 15) : 0));
   const uint32_t mod_a = (lane & 15) * (OP == kFp8Fwd ? (uint32_t)g.ssm : 1u);
   const uint32_t mod_b = OP == kFp8Fwd ? (uint32_t)(wi * (BN / WN) / 128 * KB) : lane & 15;
   v4f acc[TM][TN];
@@ -523,24 +525,46 @@ int launch(const Fp8Args& g, hipStream_t stream) {
   const int64_t mt = OP == kFp8Wgrad ? (int64_t)g.E * ceil_div64(g.N, BM) : g.R / BM + (g.E < g.R ? g.E : g.R);
   MOE355_CHECK(mt * nt < (1ll << 31), MOE355_EUNSUPPORTED);  // tiles are counted in 32 bits
   // as many workgroups as the CUs hold at a time, or tiles; more where one would get more than kMaxTiles
-  const int64_t slots = 256 * (BM == 256 ? 1 : BM == 128 ? 2 : 3), need = ceil_div64(ceil_div64(mt * nt, 8), kMaxTiles) * 8;
+  const int64_t slots = 256 * (BM == 256 ? 1 : BN == 128 ? 2 : 4), need = ceil_div64(ceil_div64(mt * nt, 8), kMaxTiles) * 8;
   const int64_t few = ceil_div64(mt * nt, 8) * 8 < slots ? ceil_div64(mt * nt, 8) * 8 : slots, grid = few > need ? few : need;
   hipLaunchKernelGGL(fn, dim3((unsigned)grid), dim3(64 * WM * WN), 0, stream, g);
   return launch_status();
 }
 
-// The tile: 256 x 256 where it makes enough work for the CUs, else 128 x 128, else 64 x 64.  The
-// offsets are on the device, so the number of row tiles is a guess: half a tile more per expert.
+// Row tiles of t rows that R rows make over E experts: the offsets are on the device, so each row is taken to fall on an
+// expert by chance (normal approximation; the number of tiles is sum_k P(rows > k t)).
+double expected_tiles(int R, int E, int t) {
+  const double a = (double)R / E, sd = sqrt(2 * a * (1 - 1.0 / E)) + 1e-9;
+  double n = 0;
+  const int64_t sure = (int64_t)((a - 3 * sd) / t);  // (3 * sqrt(2) standard deviations)
+  if (sure > 0) n = (double)sure;
+  for (int64_t k = sure > 0 ? sure : 0; (double)k * t < a + 3 * sd; ++k) n += 0.5 * erfc((k * (double)t + 0.5 - a) / sd);
+  return n * E;
+}
+
+// The tile.  Few tiles, or few rows an expert: 32 x 64 by two waves, four workgroups a CU; the weights' bytes bound the latter, and
+// what counts is how many of them are on their way.  From 13 to 40 rows an expert 64 x 128.  Beyond, the cheaper one of
+// 256 x 256, in whole rounds of the 256 CUs, and 128 x 128, whose round of 512 costs 0.715 of that.
+// Measured, us with tiles of 32 x 64 / 64 x 128 / 128 x 128 (fp32 scales):
+//   8 rows over 256 experts of 4096 x 7168 42 / 44 / 45; 512 rows over 256 of 7168 x 2048 538 / 540 / 562;
+//   32 experts of 4096 x 7168: 2 rows each on average 139 / 144 / 153, 8 rows 160 / 160 / 164, 32 rows 220 / 168 / 176,
+//   64 rows 312 / 234 / 198; 300 rows over 4 experts of 512 x 2048 (E8M0) 10.2 / 12.4 / 14.5
+// and of 128 x 128 / 256 x 256 (E8M0; wgrad in brackets):
+//   32 experts of 2048 x 2048: 128 rows each on average 35 / 33 (82 / 76), 256 rows 50 / 56 (108 / 101); 160 rows of
+//   4096 x 2048 87 / 75 (187 / 162); 2 experts of 2000 x 2000, 500 rows 15 / 26 (12.4 / 14.6); one of 4096 x 7168, 4096 rows
+//   124 / 92 (122 / 100)
 template <int OP, bool E8, bool OUT32>
 int run(const Fp8Args& g, hipStream_t stream) {
-  const int64_t cols = OP == kFp8Fwd ? g.N : g.K, parts = g.E < g.R ? g.E : g.R;
-  auto tiles = [&](int64_t t) {
-    return OP == kFp8Wgrad ? g.E * ceil_div64(g.N, t) * ceil_div64(g.K, t) : (g.R / t + (parts + 1) / 2) * ceil_div64(cols, t);
+  const int64_t cols = OP == kFp8Fwd ? g.N : g.K;
+  auto tiles = [&](int tm, int tn) {
+    return (OP == kFp8Wgrad ? (double)g.E * ceil_div64(g.N, tm) : expected_tiles(g.R, g.E, tm)) * ceil_div64(cols, tn);
   };
-  if (OP == kFp8Wgrad ? tiles(256) >= 512 : tiles(256) >= 200 && g.R >= 112ll * g.E)
-    return launch<OP, E8, OUT32, 256, 256, 4, 2>(g, stream);
-  if (tiles(128) >= 192) return launch<OP, E8, OUT32, 128, 128, 4, 2>(g, stream);
-  return launch<OP, E8, OUT32, 64, 64, 4, 1>(g, stream);
+  if constexpr (OP == kFp8Fwd) {
+    if (g.R <= 12ll * g.E || tiles(32, 64) <= 1024) return launch<OP, E8, OUT32, 32, 64, 2, 1>(g, stream);
+    if (g.R <= 40ll * g.E) return launch<OP, E8, OUT32, 64, 128, 4, 2>(g, stream);
+  }
+  if (ceil(tiles(256, 256) / 256) <= 0.715 * tiles(128, 128) / 512) return launch<OP, E8, OUT32, 256, 256, 4, 2>(g, stream);
+  return launch<OP, E8, OUT32, 128, 128, 4, 2>(g, stream);
 }
 
 bool on4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
