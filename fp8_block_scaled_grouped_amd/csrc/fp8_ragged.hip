@@ -147,44 +147,56 @@ __device__ __forceinline__ uint32_t pack16(float a, float b) {
 // Stores a wave's sums and clears them: lane l holds of tile (i, j) the row 16 i + l % 16 and the four columns from 16 j + 4 (l / 16).
 // c: the wave's first row and column; rows and cols are left from there on (fewer than none: nothing is stored).  Stores past them
 // go past the end of a buffer descriptor, so there is no branch.
-// 16-bit: pairs of column tiles change lanes so that a lane holds 8 columns, 16 bytes; fp32: so that a store covers 8 rows of
-// 128 bytes rather than 16 of 64.
-template <bool F16, bool OUT32, int TM, int TN>
+// A store covers 8 rows of 128 bytes: lanes l and l ^ 8 change tiles, and before that, with 16 bits, lanes 16 apart, so that one holds
+// 8 columns, 16 bytes.
+template <bool F16, bool OUT32, int AUX, int TM, int TN>
 __device__ __forceinline__ void store_sums(v4f (&acc)[TM][TN], void* c, int64_t ldc, int rows, int cols, int lane) {
   constexpr int kSize = OUT32 ? 4 : 2;
   const int r = min(rows, 16 * TM);
   const uint32_t ld = (uint32_t)ldc * kSize;
   const int bytes = rows > 0 && cols > 0 ? (int)((uint32_t)(r - 1) * ld) + min(cols, 16 * TN) * kSize : 0;
   const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(c, 0, bytes, 0x00020000);
+  const bool up = lane & 8;
+  // p of rows 0 .. 7 and, from lane l ^ 8, q of those; p and q of rows 8 .. 15
+  auto halves = [&](const u32x4& p, const u32x4& q, u32x4& first, u32x4& second) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t y = __builtin_amdgcn_update_dpp(0, up ? p[k] : q[k], 0x128, 0xf, 0xf, true);
+      first[k] = up ? y : p[k];
+      second[k] = up ? q[k] : y;
+    }
+  };
+  auto store = [&](const u32x4& p, const u32x4& q, int i, int n) {  // columns n of rows 16 i ..
+    u32x4 first, second;
+    halves(p, q, first, second);
+    const uint32_t at = n < cols ? (16 * i + (lane & 7)) * ld + n * kSize : kPastEnd;
+    __builtin_amdgcn_raw_buffer_store_b128(first, rsrc, at, 0, AUX);
+    __builtin_amdgcn_raw_buffer_store_b128(second, rsrc, at + 8 * ld, 0, AUX);
+  };
+  constexpr int kTiles = OUT32 ? 2 : 4;  // 128 bytes
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
 #pragma unroll
-    for (int j = 0; j < TN; j += 2) {
+    for (int j = 0; j < TN; j += kTiles) {
       if constexpr (OUT32) {
-        const bool up = lane & 8;
-        u32x4 first, second;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t p = __float_as_uint(acc[i][j][k]), q = __float_as_uint(acc[i][j + 1][k]);
-          const uint32_t y = __builtin_amdgcn_update_dpp(0, up ? p : q, 0x128, 0xf, 0xf, true);  // from lane l ^ 8
-          first[k] = up ? y : p;
-          second[k] = up ? q : y;
-        }
-        const int n = 4 * (lane >> 4) + 16 * (j + (up ? 1 : 0));
-        const uint32_t at = n < cols ? (16 * i + (lane & 7)) * ld + n * kSize : kPastEnd;
-        __builtin_amdgcn_raw_buffer_store_b128(first, rsrc, at, 0, 0);
-        __builtin_amdgcn_raw_buffer_store_b128(second, rsrc, at + 8 * ld, 0, 0);
+        store(__builtin_bit_cast(u32x4, acc[i][j]), __builtin_bit_cast(u32x4, acc[i][j + 1]), i, 4 * (lane >> 4) + 16 * (j + (up ? 1 : 0)));
       } else {
-        const v4f &x = acc[i][j], &y = acc[i][j + 1];
-        const auto lo = __builtin_amdgcn_permlane16_swap(pack16<F16>(x[0], x[1]), pack16<F16>(y[0], y[1]), false, false);
-        const auto hi = __builtin_amdgcn_permlane16_swap(pack16<F16>(x[2], x[3]), pack16<F16>(y[2], y[3]), false, false);
-        // lanes of groups 0 and 2 hold columns 0 .. 7 and 8 .. 15 of tile j, those of 1 and 3 of tile j + 1
-        const int n = 16 * (j + ((lane >> 4) & 1)) + 8 * (lane >> 5);
-        const uint32_t at = n < cols ? (16 * i + (lane & 15)) * ld + n * kSize : kPastEnd;
-        __builtin_amdgcn_raw_buffer_store_b128(u32x4{lo[0], hi[0], lo[1], hi[1]}, rsrc, at, 0, 0);
+        u32x4 v[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const v4f &x = acc[i][j + 2 * h], &y = acc[i][j + 2 * h + 1];
+          // lanes of groups 0 and 2 come to hold columns 0 .. 7 and 8 .. 15 of the one tile, those of 1 and 3 of the other
+          const auto lo = __builtin_amdgcn_permlane16_swap(pack16<F16>(x[0], x[1]), pack16<F16>(y[0], y[1]), false, false);
+          const auto hi = __builtin_amdgcn_permlane16_swap(pack16<F16>(x[2], x[3]), pack16<F16>(y[2], y[3]), false, false);
+          v[h] = u32x4{lo[0], hi[0], lo[1], hi[1]};
+        }
+        store(v[0], v[1], i, 16 * (j + (up ? 2 : 0) + ((lane >> 4) & 1)) + 8 * (lane >> 5));
       }
-      acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-      acc[i][j + 1] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < kTiles; ++k) {
+        acc[i][j + k] = v4f{0.f, 0.f, 0.f, 0.f};
+        if constexpr (OUT32) asm volatile("" : "+v"(acc[i][j + k]));  // else the compiler keeps what was stored as well
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
   }
@@ -208,6 +220,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_ragged_kernel(Fp8Args g) 
   constexpr int kAhead = TM * TN >= 32 ? 1 : 2, kHold = 2 * kAhead, kHalf = TN / 2;  // fragments of B ahead, and held
   constexpr int kABytes = BM * 128, kHBytes = BN * 64;  // a slot of A, a half of B
   constexpr int NA = kABytes / 1024 / NW, NH = kHBytes / 1024 / NW;  // DMAs of a wave
+  // wgrad's sums are stored past the caches (1.08 ms against 0.99, 32768 rows over 32 experts of 4096 x 7168; 218 us against
+  // 177, 16384 over 32 of 4096 x 2048; fwd's, which the next product reads, 0.81 either way)
+  constexpr int kAux = OP == kFp8Wgrad ? 2 : 0, kBand = OP == kFp8Wgrad ? 4 : 8;
   constexpr int kWinA = (BM + 63) / 64, kWin = kWinA + BN / 64;  // windows of 64 scales: A's rows, then B's columns
   constexpr int kScales = 256 * kWin;                    // scales of a step, a dword each
   static_assert(NA * NW * 1024 == kABytes && NH * NW * 1024 == kHBytes && NW >= kWin && TN >= 4 && TN % 4 == 0, "whole DMAs");
@@ -243,9 +258,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_ragged_kernel(Fp8Args g) 
         m = mtiles;
       }
       segment(g.offsets, g.R, e, lo, hi);
-      // inside an expert the tiles advance in bands of 8 row tiles: those that an XCD works on at a time share few panels
-      const int rest = (int)t - base * ntiles, band = 8 * ntiles, b0 = max(0, rest) / band * 8, in = max(0, rest) % band;
-      const int height = max(1, min(8, m - b0)), mt = b0 + in % height;
+      // inside an expert the tiles advance in bands of row tiles: those that an XCD works on at a time share few panels
+      const int rest = (int)t - base * ntiles, band = kBand * ntiles, b0 = max(0, rest) / band * kBand, in = max(0, rest) % band;
+      const int height = max(1, min(kBand, m - b0)), mt = b0 + in % height;
       const bool known = rest >= 0 && mt < m;  // always, unless the offsets decrease
       const int m0 = known ? mt * BM : 0, n0 = in / height * BN;
       const int left = !known ? 0 : OP == kFp8Fwd ? hi - lo - m0 : g.N - m0, mrows = min(BM, left), nrows = min(BN, ndim - n0);
@@ -386,7 +401,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_ragged_kernel(Fp8Args g) 
 #pragma unroll
       for (int i = 0; i < NH; ++i) dma_b(h, i, hb[2 * s + h]);
   }
-  vm_wait<NA + 1 + 2 * NH>();
+  vm_wait<0>();  // both steps: no stores stand behind the second's DMAs yet, as the first wait of a tile takes for granted
   barrier_only();
   v8i ra[2][TM], rb[kHold];
   uint32_t rawa[TM], rawb[kHold];  // scales of A's fragments (this step's, then the next one's) and of B's held ones
@@ -401,8 +416,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_ragged_kernel(Fp8Args g) 
     rawb[j] = read_u32(sc + atsb + (OP == kFp8Wgrad ? 64 * j : 0));
   }
 
-  auto step = [&](auto par_c) __attribute__((always_inline)) {
-    constexpr int PAR = decltype(par_c)::value;
+  // first: of a tile, so the stores of the last one's sums are behind the DMAs that row TN/2 waits for and may be under way
+  auto step = [&](auto par_c, auto first_c) __attribute__((always_inline)) {
+    constexpr int PAR = decltype(par_c)::value, kLate = decltype(first_c)::value ? TM * TN / (OUT32 ? 2 : 4) * 2 : 0;
     // a byte's place in its dword is the same for all of a lane's rows (16 apart), and for its columns
     const uint32_t sha = E8 ? 8 * ((mod_a + rema[0]) & 3) : 0, shb = E8 ? 8 * ((mod_b + remb[0]) & 3) : 0;
     uint32_t sa[TM];
@@ -421,7 +437,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_ragged_kernel(Fp8Args g) 
         next_a();
       }
       if (j == kHalf) {
-        vm_wait<NA + 1>();
+        vm_wait<NA + 1 + kLate>();
         barrier_only();
         next_b();
       }
@@ -491,28 +507,35 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_ragged_kernel(Fp8Args g) 
   };
   for (int t = 0; t < count; ++t) {
     int left = uniform(tiles[t].steps);
-    for (; left >= 2; left -= 2) {
+    using Even = std::integral_constant<int, 0>;
+    using Odd = std::integral_constant<int, 1>;
+    if (left > 0) {
       if (fs == fsteps) seek();
-      step(std::integral_constant<int, 0>{});
-      if (fs == fsteps) seek();
-      step(std::integral_constant<int, 1>{});
-    }
-    if (left) {
-      if (fs == fsteps) seek();
-      step(std::integral_constant<int, 0>{});
+      step(Even{}, Odd{});
+      for (--left; left >= 2; left -= 2) {
+        if (fs == fsteps) seek();
+        step(Odd{}, Even{});
+        if (fs == fsteps) seek();
+        step(Even{}, Even{});
+      }
+      if (left) {
+        if (fs == fsteps) seek();
+        step(Odd{}, Even{});
+      } else {
 #pragma unroll
-      for (int i = 0; i < TM; ++i) ra[0][i] = ra[1][i];
-      const uint32_t was = sl[0];
-      sl[0] = sl[1];
-      sl[1] = was;
+        for (int i = 0; i < TM; ++i) ra[0][i] = ra[1][i];
+        const uint32_t was = sl[0];
+        sl[0] = sl[1];
+        sl[1] = was;
+      }
     }
     const int64_t row0 = uniform64(tiles[t].row0);
     const int mrows = uniform(tiles[t].mrows), n0 = uniform(tiles[t].n0);
     int l = lane;
     asm volatile("" : "+v"(l));  // the stores' addresses are made here, not kept in registers through the steps
     uint8_t* c = static_cast<uint8_t*>(g.c) + ((row0 + wm) * g.ldc + n0 + wi * (BN / WN)) * (OUT32 ? 4 : 2);
-    if (OUT32 || !g.f16) store_sums<false, OUT32>(acc, c, g.ldc, mrows - wm, ndim - n0 - wi * (BN / WN), l);
-    else store_sums<true, false>(acc, c, g.ldc, mrows - wm, ndim - n0 - wi * (BN / WN), l);
+    if (OUT32 || !g.f16) store_sums<false, OUT32, kAux>(acc, c, g.ldc, mrows - wm, ndim - n0 - wi * (BN / WN), l);
+    else store_sums<true, false, kAux>(acc, c, g.ldc, mrows - wm, ndim - n0 - wi * (BN / WN), l);
   }
   vm_wait<0>();
 }
