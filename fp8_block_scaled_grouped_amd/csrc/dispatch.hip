@@ -19,83 +19,112 @@ namespace {
 constexpr int kMaxE = 1024;
 
 // ------------------------------------------------------------------ moe_group
-// Chunk c of the pairs (all of them with one chunk) by one workgroup of W waves, each with a
-// contiguous part.  counts: [chunks][E] histograms of the chunks, or NULL with one chunk.
+constexpr int kWaves = 16;                   // of a workgroup
+constexpr int kThreads = 64 * kWaves;
+constexpr int kOneChunk = 4096;              // up to here one workgroup takes all pairs
+constexpr int kMaxChunks = 256;
+
+// Where pair p's id stands: ids are dense (ld = 0) or in rows of k, ld apart.
+__device__ __forceinline__ int expert_of(const int32_t* ids, int64_t ld, uint32_t k, int E, uint32_t p) {
+  const int e = ids[ld == 0 ? (int64_t)p : (int64_t)(p / k) * ld + p % k];
+  return e >= 0 && e < E ? e : -1;
+}
+
+__global__ __launch_bounds__(kThreads) void group_count_kernel(const int32_t* __restrict__ ids, int64_t ld, int k, uint32_t n,
+                                                               int E, uint32_t chunk, int32_t* __restrict__ counts) {
+  __shared__ int hist[kMaxE];
+  for (int e = threadIdx.x; e < E; e += kThreads) hist[e] = 0;
+  __syncthreads();
+  const uint32_t c0 = blockIdx.x * chunk, c1 = min(n, c0 + chunk);
+  for (uint32_t p = c0 + threadIdx.x; p < c1; p += kThreads) {
+    const int e = expert_of(ids, ld, k, E, p);
+    if (e >= 0) atomicAdd(&hist[e], 1);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += kThreads) counts[(int64_t)blockIdx.x * E + e] = hist[e];
+}
+
+// Chunk blockIdx.x of the pairs (all of them with one chunk), each wave a contiguous part.  counts: [chunks][E] histograms of the
+// chunks, or NULL with one chunk.
 // A wave counts its part's experts in LDS; prefixes over waves, chunks and experts give each wave the first row of
 // every expert, and a second walk over the part ranks each pair among the 64 at hand: ballots over the bits
 // of the expert find the lanes with the same one, and the lowest of them moves the expert's next row on.
-template <int W>
-__global__ __launch_bounds__(64 * W) void group_kernel(const int32_t* __restrict__ ids, int64_t ld, int k, int64_t n, int E,
-                                                       int bits, int64_t chunk, const int32_t* __restrict__ counts,
-                                                       int32_t* __restrict__ offsets, int32_t* __restrict__ row_of_pair,
-                                                       int32_t* __restrict__ pair_of_row) {
-  extern __shared__ int next[];  // [W][E], then 16 sums of waves and the total
-  int* wsum = next + W * E;
+// Bound by latency: 64 tokens x 8 of 256 experts, one launch, 4 us; 8192 tokens x 8, two launches of 16 workgroups, @@ us (with chunks
+// of 1024 pairs and their counts added one by one 25).
+__global__ __launch_bounds__(kThreads) void group_kernel(const int32_t* __restrict__ ids, int64_t ld, int k, uint32_t n, int E,
+                                                         int bits, uint32_t chunk, const int32_t* __restrict__ counts,
+                                                         int32_t* __restrict__ offsets, int32_t* __restrict__ row_of_pair,
+                                                         int32_t* __restrict__ pair_of_row) {
+  extern __shared__ int next[];  // [kWaves][E], then the sums of the waves
+  int* wsum = next + kWaves * E;
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-  const int64_t c0 = (int64_t)blockIdx.x * chunk, c1 = c0 + chunk < n ? c0 + chunk : n;
-  const int64_t part = (chunk / W + 63) / 64 * 64;
-  const int64_t p0 = c0 + w * part < c1 ? c0 + w * part : c1, p1 = p0 + part < c1 ? p0 + part : c1;
-  auto expert = [&](int64_t p) {
-    if (p >= p1) return -1;
-    const int64_t t = p / k;
-    const int e = ids[t * ld + (p - t * k)];
-    return e >= 0 && e < E ? e : -1;
-  };
-  for (int i = tid; i < W * E; i += 64 * W) next[i] = 0;
+  const uint32_t c0 = blockIdx.x * chunk, c1 = min(n, c0 + chunk), part = (chunk / kWaves + 63) / 64 * 64;
+  const uint32_t p0 = min(c1, c0 + w * part), p1 = min(c1, p0 + part);
+  // the ids of a part of up to 256 pairs stay in registers
+  constexpr int kHeld = kOneChunk / kThreads;
+  int held[kHeld];
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) held[i] = p0 + 64 * i + lane < p1 ? expert_of(ids, ld, k, E, p0 + 64 * i + lane) : -1;
+  for (int i = tid; i < kWaves * E; i += kThreads) next[i] = 0;
   __syncthreads();
-  for (int64_t p = p0; p < p1; p += 64) {
-    const int e = expert(p + lane);
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i)
+    if (held[i] >= 0) atomicAdd(&next[w * E + held[i]], 1);
+  for (uint32_t p = p0 + 64 * kHeld + lane; p < p1; p += 64) {
+    const int e = expert_of(ids, ld, k, E, p);
     if (e >= 0) atomicAdd(&next[w * E + e], 1);
   }
   __syncthreads();
-  // per expert: rows in all chunks, and in the chunks before this one; then the scan over experts
-  int carry = 0;
-  for (int e0 = 0; e0 < E; e0 += 64 * W) {
-    const int e = e0 + tid;
-    int total = 0, before = 0;
-    if (e < E) {
-      if (counts) {
-        for (int c = 0; c < (int)gridDim.x; ++c) {
-          const int v = counts[(int64_t)c * E + e];
-          total += v;
-          before += c < (int)blockIdx.x ? v : 0;
-        }
-      } else {
-        for (int i = 0; i < W; ++i) total += next[i * E + e];
-      }
-    }
-    int upto = total;
+  // per expert: rows in all chunks, and in the chunks before this one; then the scan over experts (at most one a thread)
+  const int e = tid;
+  int total = 0, before = 0;
+  if (e < E) {
+    if (counts) {
+      constexpr int kBatch = 16;  // loads on their way at a time
+      for (int b = 0; b < (int)gridDim.x; b += kBatch) {
+        int v[kBatch];
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int v = __shfl_up(upto, o, 64);
-      if (lane >= o) upto += v;
-    }
-    if (lane == 63) wsum[w] = upto;
-    __syncthreads();
-    int base = carry, all = 0;
-    for (int i = 0; i < W; ++i) {
-      base += i < w ? wsum[i] : 0;
-      all += wsum[i];
-    }
-    base += upto - total;
-    if (e < E) {
-      if (blockIdx.x == 0) {
-        offsets[e] = base;
-        if (e == E - 1) offsets[E] = base + total;
+        for (int i = 0; i < kBatch; ++i) v[i] = b + i < (int)gridDim.x ? counts[(int64_t)(b + i) * E + e] : 0;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          total += v[i];
+          before += b + i < (int)blockIdx.x ? v[i] : 0;
+        }
       }
-      int at = base + before;
-      for (int i = 0; i < W; ++i) {
-        const int v = next[i * E + e];
-        next[i * E + e] = at;
-        at += v;
-      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWaves; ++i) total += next[i * E + e];
     }
-    carry += all;
-    __syncthreads();
   }
-  for (int64_t q = p0; q < p1; q += 64) {
-    const int64_t p = q + lane;
-    const int e = expert(p);
+  int upto = total;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int v = __shfl_up(upto, o, 64);
+    if (lane >= o) upto += v;
+  }
+  if (lane == 63) wsum[w] = upto;
+  __syncthreads();
+  int base = upto - total, all = 0;
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) {
+    base += i < w ? wsum[i] : 0;
+    all += wsum[i];
+  }
+  if (e < E) {
+    if (blockIdx.x == 0) {
+      offsets[e] = base;
+      if (e == E - 1) offsets[E] = all;
+    }
+    int at = base + before;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) {
+      const int v = next[i * E + e];
+      next[i * E + e] = at;
+      at += v;
+    }
+  }
+  __syncthreads();
+  auto place = [&](int e, uint32_t p) {
     unsigned long long same = __ballot(e >= 0);
     for (int b = 0; b < bits; ++b) {
       const unsigned long long set = __ballot((e >> b) & 1);
@@ -113,33 +142,17 @@ __global__ __launch_bounds__(64 * W) void group_kernel(const int32_t* __restrict
       row_of_pair[p] = row;
       if (pair_of_row && row >= 0) pair_of_row[row] = (int)p;
     }
-  }
+  };
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i)
+    if (p0 + 64 * i < p1) place(held[i], p0 + 64 * i + lane);
+  for (uint32_t q = p0 + 64 * kHeld; q < p1; q += 64) place(q + lane < p1 ? expert_of(ids, ld, k, E, q + lane) : -1, q + lane);
   if (pair_of_row)  // rows behind the last segment
-    for (int64_t r = carry + (int64_t)blockIdx.x * (64 * W) + tid; r < n; r += (int64_t)gridDim.x * (64 * W)) pair_of_row[r] = -1;
+    for (uint32_t r = all + blockIdx.x * kThreads + tid; r < n; r += gridDim.x * kThreads) pair_of_row[r] = -1;
 }
 
-__global__ __launch_bounds__(256) void group_count_kernel(const int32_t* __restrict__ ids, int64_t ld, int k, int64_t n,
-                                                          int E, int64_t chunk, int32_t* __restrict__ counts) {
-  __shared__ int hist[kMaxE];
-  for (int e = threadIdx.x; e < E; e += 256) hist[e] = 0;
-  __syncthreads();
-  const int64_t c0 = (int64_t)blockIdx.x * chunk, c1 = c0 + chunk < n ? c0 + chunk : n;
-  for (int64_t p = c0 + threadIdx.x; p < c1; p += 256) {
-    const int64_t t = p / k;
-    const int e = ids[t * ld + (p - t * k)];
-    if (e >= 0 && e < E) atomicAdd(&hist[e], 1);
-  }
-  __syncthreads();
-  for (int e = threadIdx.x; e < E; e += 256) counts[(int64_t)blockIdx.x * E + e] = hist[e];
-}
-
-constexpr int kOneChunk = 4096;   // up to here one workgroup of 16 waves takes all pairs
-constexpr int kMaxChunks = 256;
-
-inline int64_t chunk_of(int64_t n) {
-  const int64_t c = ceil_div64(ceil_div64(n, kMaxChunks), 1024) * 1024;
-  return n <= kOneChunk ? ceil_div64(n, 1024) * 1024 : c;
-}
+// Chunks of 4096 pairs, longer ones where there would be more than kMaxChunks.
+inline int64_t chunk_of(int64_t n) { return ceil_div64(n > 0 ? ceil_div64(n, kMaxChunks) : 1, kOneChunk) * kOneChunk; }
 
 // ------------------------------------------------------------------ rows
 template <int BYTES>
@@ -326,17 +339,14 @@ extern "C" int moe_group(const int32_t* topk_ids, int64_t ld_topk, int T, int to
                MOE355_EMISALIGNED);
   int bits = 0;
   while ((1 << bits) < E) ++bits;
-  const int64_t chunk = chunk_of(n);
-  if (n <= kOneChunk) {
-    hipLaunchKernelGGL(group_kernel<16>, dim3(1), dim3(1024), (16 * E + 32) * 4, stream, topk_ids, ld_topk, topk, n, E, bits,
-                       chunk, nullptr, offsets, row_of_pair, pair_of_row);
-    return launch_status();
-  }
-  int32_t* counts = static_cast<int32_t*>(workspace);
-  const unsigned chunks = (unsigned)ceil_div64(n, chunk);
-  hipLaunchKernelGGL(group_count_kernel, dim3(chunks), dim3(256), 0, stream, topk_ids, ld_topk, topk, n, E, chunk, counts);
-  hipLaunchKernelGGL(group_kernel<4>, dim3(chunks), dim3(256), (4 * E + 32) * 4, stream, topk_ids, ld_topk, topk, n, E, bits,
-                     chunk, counts, offsets, row_of_pair, pair_of_row);
+  const uint32_t chunk = (uint32_t)chunk_of(n);
+  const unsigned chunks = n <= kOneChunk ? 1 : (unsigned)ceil_div64(n, chunk);
+  const int64_t ld = ld_topk == topk ? 0 : ld_topk;
+  int32_t* counts = chunks > 1 ? static_cast<int32_t*>(workspace) : nullptr;
+  if (counts)
+    hipLaunchKernelGGL(group_count_kernel, dim3(chunks), dim3(kThreads), 0, stream, topk_ids, ld, topk, (uint32_t)n, E, chunk, counts);
+  hipLaunchKernelGGL(group_kernel, dim3(chunks), dim3(kThreads), (kWaves * E + kWaves) * 4, stream, topk_ids, ld, topk, (uint32_t)n, E,
+                     bits, chunk, counts, offsets, row_of_pair, pair_of_row);
   return launch_status();
 }
 

@@ -8,6 +8,7 @@ A missing library raises at the first call -- there is no fallback.
 Function names and argument order follow include/moe355.h.
 """
 import ctypes
+import functools
 import os
 
 import torch
@@ -661,33 +662,37 @@ _ELEM = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2, torch.uint8: 3}
 
 
 def _elem(t, name, most=2):
-    """The library's number of a device tensor's element type, among the first `most + 1`."""
+    """The library's number of a tensor's element type, among the first `most + 1`."""
     n = _ELEM.get(t.dtype, 9)
-    if n > most or not t.is_cuda:
-        raise ValueError("%s must be a bf16, fp16 or fp32%s GPU tensor, got %s on %s"
-                         % (name, " or uint8" if most == 3 else "", t.dtype, t.device))
+    if n > most:
+        raise ValueError("%s must be bf16, fp16 or fp32%s, got %s" % (name, " or uint8" if most == 3 else "", t.dtype))
     return n
 
 
-def _here(*tensors):
-    """The kernels are queued on the current GPU's stream: every tensor has to be on that GPU."""
+def _queue(*tensors):
+    """The current GPU's stream, on which the kernels are queued: every tensor has to be on that GPU."""
     dev = torch._C._cuda_getDevice()
     for t in tensors:
-        if t is not None and t.device.index != dev:
+        if t is not None and t.get_device() != dev:
             raise ValueError("tensors must be on the current GPU (cuda:%d), got one on %s" % (dev, t.device))
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _pairs(row_of_pair):
-    if row_of_pair.dim() != 2 or row_of_pair.shape[1] < 1:
-        raise ValueError("row_of_pair must be [T, topk]")
-    _need(row_of_pair, row_of_pair.shape, torch.int32, "row_of_pair")
+    if row_of_pair.dtype != torch.int32 or row_of_pair.dim() != 2 or row_of_pair.shape[1] < 1 or not row_of_pair.is_contiguous():
+        raise ValueError("row_of_pair must be a contiguous int32 tensor [T, topk], got %s %s" % (row_of_pair.dtype,
+                                                                                               tuple(row_of_pair.shape)))
     return row_of_pair.shape
 
 
 def _grad_wanted(*tensors):
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+    for t in tensors:
+        if t is not None and t.requires_grad:
+            return torch.is_grad_enabled()
+    return False
 
 
+@functools.lru_cache(maxsize=256)
 def moe_group_workspace(T, topk, E):
     """Bytes of workspace that moe_group needs (host-only)."""
     b = ctypes.c_size_t()
@@ -701,19 +706,21 @@ def moe_group(topk_ids, E, out=None, workspace=None):
     topk_ids int32 [T, topk] (rows may be strided).  The pairs of expert e get rows [offsets[e], offsets[e+1])
     in ascending order; pairs whose id is outside [0, E) get row -1, and rows at or past offsets[E] pair -1.
     """
-    _dev(topk_ids, torch.int32, "topk_ids")
+    if topk_ids.dtype != torch.int32:
+        raise ValueError("topk_ids must be int32, got %s" % topk_ids.dtype)
     ld = _ld(topk_ids, "topk_ids")
     T, k = topk_ids.shape
     if out is None:
-        out = (topk_ids.new_empty(E + 1), topk_ids.new_empty((T, k)), topk_ids.new_empty(T * k))
-    offsets, row_of_pair, pair_of_row = out
-    for t, shape, name in ((offsets, (E + 1,), "offsets"), (row_of_pair, (T, k), "row_of_pair"), (pair_of_row, (T * k,), "pair_of_row")):
-        _need(t, shape, torch.int32, name)
+        offsets, row_of_pair, pair_of_row = topk_ids.new_empty(E + 1), topk_ids.new_empty((T, k)), topk_ids.new_empty(T * k)
+    else:
+        offsets, row_of_pair, pair_of_row = out
+        for t, shape, name in ((offsets, (E + 1,), "offsets"), (row_of_pair, (T, k), "row_of_pair"), (pair_of_row, (T * k,), "pair_of_row")):
+            _need(t, shape, torch.int32, name)
     if workspace is None and T * k > 4096:
         workspace = topk_ids.new_empty(moe_group_workspace(T, k, E), dtype=torch.uint8)
-    _here(topk_ids, offsets, row_of_pair, pair_of_row, workspace)
+    stream = _queue(topk_ids, *out or (), workspace)
     ws, wsn = (None, 0) if workspace is None else (_ptr(_dev(workspace, torch.uint8, "workspace")), workspace.numel())
-    _check(lib().moe_group(_ptr(topk_ids), ld, T, k, E, _ptr(offsets), _ptr(row_of_pair), _ptr(pair_of_row), ws, wsn, _stream()))
+    _check(lib().moe_group(_ptr(topk_ids), ld, T, k, E, _ptr(offsets), _ptr(row_of_pair), _ptr(pair_of_row), ws, wsn, stream))
     return offsets, row_of_pair, pair_of_row
 
 
@@ -744,12 +751,11 @@ def moe_dispatch(x, row_of_pair, rows=None):
     H = x.shape[1]
     if rows is None:
         rows = x.new_empty((T * k, H))
-    elif rows.dim() != 2 or rows.shape[1] != H:
-        raise ValueError("rows must be [R, %d]" % H)
-    _dev(rows, x.dtype, "rows")
-    _here(x, row_of_pair, rows)
+    elif rows.dim() != 2 or rows.shape[1] != H or rows.dtype != x.dtype:
+        raise ValueError("rows must be [R, %d] in the type of x" % H)
+    stream = _queue(x, row_of_pair, rows)
     _check(lib().moe_dispatch(_ptr(x), dt, _ld(x, "x"), T, H, k, _ptr(row_of_pair), rows.shape[0], _ptr(rows), _ld(rows, "rows"),
-                              _stream()))
+                              stream))
     return rows
 
 
@@ -768,9 +774,8 @@ class _Combine(torch.autograd.Function):
 
 
 def _routing_weights(weights, T, k):
-    _dev(weights, torch.float32, "weights")
-    if weights.shape != (T, k):
-        raise ValueError("weights must be %s, got %s" % ((T, k), tuple(weights.shape)))
+    if weights.dtype != torch.float32 or weights.shape != (T, k):
+        raise ValueError("weights must be fp32 %s, got %s %s" % ((T, k), weights.dtype, tuple(weights.shape)))
     return _ld(weights, "weights")
 
 
@@ -789,9 +794,9 @@ def moe_combine(rows, row_of_pair, weights=None, out=None):
     R, H = rows.shape
     ld_w = 0 if weights is None else _routing_weights(weights, T, k)
     out = _out(out, (T, H), rows.dtype, rows, "out")
-    _here(rows, row_of_pair, weights, out)
+    stream = _queue(rows, row_of_pair, weights, out)
     _check(lib().moe_combine(_ptr(rows), dt, _ld(rows, "rows"), T, H, k, _ptr(row_of_pair), R, _ptr(weights), ld_w, _ptr(out),
-                             _ld(out, "out"), _stream()))
+                             _ld(out, "out"), stream))
     return out
 
 
@@ -806,16 +811,20 @@ def moe_combine_grad(dout, rows, row_of_pair, weights, drows=None, dweights=None
     if rows.dim() != 2:
         raise ValueError("rows must be [R, H]")
     R, H = rows.shape
-    _dev(dout, rows.dtype, "dout")
-    if dout.shape != (T, H):
-        raise ValueError("dout must be %s, got %s" % ((T, H), tuple(dout.shape)))
+    if dout.shape != (T, H) or dout.dtype != rows.dtype:
+        raise ValueError("dout must be %s %s, got %s %s" % (rows.dtype, (T, H), dout.dtype, tuple(dout.shape)))
     ld_w = _routing_weights(weights, T, k)
     drows = _out(drows, (R, H), rows.dtype, rows, "drows") if want[0] else None
-    dweights = _need(_out(dweights, (T, k), torch.float32, weights, "dweights"), (T, k), torch.float32, "dweights") if want[1] else None
-    _here(dout, rows, row_of_pair, weights, drows, dweights)
+    if not want[1]:
+        dweights = None
+    elif dweights is None:
+        dweights = weights.new_empty((T, k))
+    else:
+        _need(dweights, (T, k), torch.float32, "dweights")
+    stream = _queue(dout, rows, row_of_pair, weights, drows, dweights)
     _check(lib().moe_combine_grad(_ptr(dout), _ld(dout, "dout"), _ptr(rows), _ld(rows, "rows"), dt, T, H, k, _ptr(row_of_pair), R,
                                   _ptr(weights), ld_w, _ptr(drows), 0 if drows is None else _ld(drows, "drows"), _ptr(dweights),
-                                  _stream()))
+                                  stream))
     return drows, dweights
 
 
@@ -852,9 +861,9 @@ def fp8_quant_ragged(x, offsets=None, rows=True, columns=True):
         qt, tscale = x.new_empty((blocks, K, 128), dtype=torch.uint8), x.new_empty((blocks, K), dtype=torch.uint8)
     if q is None and qt is None:
         raise ValueError("neither rows nor columns asked for (columns need offsets)")
-    _here(x, offsets)
+    stream = _queue(x, offsets)
     _check(lib().fp8_quant_ragged(_ptr(x), f16, ld, _ptr(offsets), R, E, K, _ptr(q), K, _ptr(scale), 1, R, _ptr(qt), _ptr(tscale),
-                                  _stream()))
+                                  stream))
     return q, scale, qt, tscale
 
 
@@ -875,9 +884,9 @@ def fp8_quant_128x128(w, scale_format="e8m0", transposed=False):
     qt = tscale = None
     if transposed:
         qt, tscale = w.new_empty((E, K, N), dtype=torch.uint8), w.new_empty((E, _nblk(K), _nblk(N)), dtype=sdt)
-    _here(w)
+    stream = _queue(w)
     _check(lib().fp8_quant_128x128(_ptr(w), f16, E, N, K, _ptr(q), _ptr(scale), _ptr(qt), _ptr(tscale), int(scale_format == "e8m0"),
-                                   _stream()))
+                                   stream))
     return (q, scale, qt, tscale) if transposed else (q, scale)
 
 
@@ -889,24 +898,29 @@ def grouped_gemm_fp8(x8, x_scale, w8, w_scale, offsets, y=None, out_dtype=torch.
     ceil(K/128)], both fp32 (fp8_quant_1x128, checkpoints) or both uint8 for E8M0 (fp8_quant_ragged, fp8_quant_128x128).
     Not differentiable (grouped_linear_fp8 is).
     """
-    _dev(x8, torch.uint8, "x8")
+    if x8.dtype != torch.uint8 or w8.dtype != torch.uint8:
+        raise ValueError("x8 and w8 must be uint8, got %s and %s" % (x8.dtype, w8.dtype))
     ld = _ld(x8, "x8")
     R, K = x8.shape
-    E, N, _ = w8.shape
-    _need(w8, (E, N, K), torch.uint8, "w8")
-    e8m0 = _fp4_scale(w_scale, (E, _nblk(N), _nblk(K)), "w_scale")
-    _dev(x_scale, w_scale.dtype, "x_scale")
+    E, N, wK = w8.shape
+    NB, KB = _nblk(N), _nblk(K)
+    if wK != K or not w8.is_contiguous():
+        raise ValueError("w8 must be a contiguous [E, N, %d], got %s" % (K, tuple(w8.shape)))
+    e8m0 = int(w_scale.dtype == torch.uint8)
+    if w_scale.dtype not in (torch.uint8, torch.float32) or w_scale.shape != (E, NB, KB) or not w_scale.is_contiguous():
+        raise ValueError("w_scale must be a contiguous fp32 or uint8 %s, got %s %s" % ((E, NB, KB), w_scale.dtype, tuple(w_scale.shape)))
     if scale_layout == "kblock":
         x_scale = x_scale.t()
     elif scale_layout != "row":
         raise ValueError("scale_layout must be 'row' or 'kblock'")
-    if x_scale.shape != (R, _nblk(K)):
-        raise ValueError("x_scale must have shape %s, got %s" % ((R, _nblk(K)), tuple(x_scale.shape)))
-    _need(offsets, (E + 1,), torch.int32, "offsets")
+    if x_scale.shape != (R, KB) or x_scale.dtype != w_scale.dtype:
+        raise ValueError("x_scale must be %s %s, got %s %s" % (w_scale.dtype, (R, KB), x_scale.dtype, tuple(x_scale.shape)))
+    if offsets.dtype != torch.int32 or offsets.shape != (E + 1,) or not offsets.is_contiguous():
+        raise ValueError("offsets must be a contiguous int32 tensor of %d, got %s %s" % (E + 1, offsets.dtype, tuple(offsets.shape)))
     y = _out(y, (R, N), out_dtype if y is None else y.dtype, x8, "y")
-    _here(x8, x_scale, w8, w_scale, offsets, y)
+    stream = _queue(x8, x_scale, w8, w_scale, offsets, y)
     _check(lib().grouped_gemm_fp8(_ptr(x8), _ptr(x_scale), ld, x_scale.stride(0), x_scale.stride(1), _ptr(w8), _ptr(w_scale), e8m0,
-                                  _ptr(offsets), R, E, N, K, _ptr(y), _ld(y, "y"), _half(y, "y"), _stream()))
+                                  _ptr(offsets), R, E, N, K, _ptr(y), _ld(y, "y"), _half(y, "y"), stream))
     return y
 
 
@@ -921,9 +935,9 @@ def grouped_gemm_fp8_wgrad(dyt, dyt_scale, xt, xt_scale, offsets, R, dw=None, ou
         _need(t, shape, torch.uint8, name)
     dt = out_dtype if dw is None else dw.dtype
     dw = _need(_out(dw, (E, N, K), dt, dyt, "dw"), (E, N, K), dt, "dw")
-    _here(dyt, dyt_scale, xt, xt_scale, offsets, dw)
+    stream = _queue(dyt, dyt_scale, xt, xt_scale, offsets, dw)
     _check(lib().grouped_gemm_fp8_wgrad(_ptr(dyt), _ptr(dyt_scale), _ptr(xt), _ptr(xt_scale), _ptr(offsets), R, E, N, K, _ptr(dw),
-                                        _elem(dw, "dw"), _stream()))
+                                        _elem(dw, "dw"), stream))
     return dw
 
 

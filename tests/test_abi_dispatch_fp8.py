@@ -25,7 +25,7 @@ def test_group_codes(L):
         return L.moe_group_workspace(T, k, E, ctypes.byref(n))
 
     assert size() == 0 and n.value == 0 and size(T=512, k=8) == 0 and n.value == 0
-    assert size(T=513, k=8, E=256) == 0 and n.value == 5 * 256 * 4
+    assert size(T=513, k=8, E=256) == 0 and n.value == 2 * 256 * 4
     assert size(T=1 << 20, k=8, E=1024) == 0 and n.value == 256 * 1024 * 4
     assert size(T=-1) == -1 and size(k=0) == -1 and size(E=0) == -1 and size(E=1025) == -2 and size(T=1 << 28, k=8) == -2
     assert L.moe_group_workspace(1, 1, 1, None) == -1
@@ -35,7 +35,7 @@ def test_group_codes(L):
 
     assert group(ids=None) == -1 and group(off=None) == -1 and group(rop=None) == -1 and group(ld=1) == -1
     assert group(E=1025) == -2 and group(T=-1) == -1
-    assert group(T=5000) == -1 and group(T=5000, ws=_p(), wsn=64) == -1 and group(T=5000, ws=_p(2), wsn=1 << 20) == -3
+    assert group(T=5000) == -1 and group(T=5000, ws=_p(), wsn=32) == -1 and group(T=5000, ws=_p(2), wsn=1 << 20) == -3
     assert group(ids=_p(2)) == -3 and group(off=_p(2)) == -3 and group(rop=_p(1)) == -3 and group(por=_p(1)) == -3
 
 
