@@ -58,7 +58,7 @@ def test_rows_codes(L):
     assert comb(w=_p(), ldw=1) == -1 and grad(ldw=1) == -1 and grad(w=None) == -1 and grad(ldd=7) == -1
     assert comb(w=_p(2)) == -3 and grad(w=_p(2)) == -3 and grad(d=_p(1)) == -3 and grad(dw=_p(2)) == -3
     assert grad(d=None, dw=None) == 0 and disp(R=0, rows=None) == 0 and disp(H=0, x=None) == 0
-    assert disp(T=2 ** 31 - 1, H=65536, ldx=65536, ldr=65536) == -2 and grad(T=1 << 24) == -2
+    assert disp(T=2 ** 31 - 1, H=65536, ldx=65536, ldr=65536) == -2 and grad(T=1 << 25) == -2
 
 
 def test_quant_codes(L):
