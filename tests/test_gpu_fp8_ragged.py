@@ -492,3 +492,43 @@ def test_row_offsets_past_two_to_the_32(m):
     ws[2] = 128
     y = m.grouped_gemm_fp8(x8, xs, w8, ws, _dev(off))
     assert (y[:R - 260] == 0).all() and (y[R - 260:R - 130] == K).all() and (y[R - 130:R - 1] == 2 * K).all() and (y[R - 1] == 0).all()
+
+
+class _Guarded:
+    """A tensor inside a larger allocation whose other bytes must stay."""
+
+    def __init__(self, shape, dtype):
+        n = int(np.prod(shape)) * torch.empty((), dtype=dtype).element_size()
+        self.base, self.n = torch.full((n + 2048,), 0xA5, dtype=torch.uint8, device=DEV), n
+        self.t = self.base[1024:1024 + n].view(dtype).view(shape)
+
+    def intact(self):
+        return bool((self.base[:1024] == 0xA5).all()) and bool((self.base[1024 + self.n:] == 0xA5).all())
+
+
+@pytest.mark.parametrize("counts,N,K", [([1], 8, 16), ([3, 0, 17, 64], 136, 272), ([400, 130, 129, 300], 2600, 400), ([1300, 1260], 5128, 144),
+                                        ([30, 41, 0, 38] * 16, 264, 1040), ([7, 0, 140] * 8, 264, 272)])
+def test_outputs_stay_inside_their_buffers(m, counts, N, K):
+    E, off = len(counts), _offsets(counts)
+    R = off[-1]
+    g = torch.Generator().manual_seed(N)
+    code = lambda *s: torch.randint(0, 0x7f, s, generator=g, dtype=torch.uint8).to(DEV)
+    for e8 in (True, False):
+        one = lambda *s: torch.full(s, 127 if e8 else 1, dtype=torch.uint8 if e8 else torch.float32, device=DEV)
+        y = _Guarded((R, N), torch.bfloat16)
+        m.grouped_gemm_fp8(code(R, K), one(R, -(-K // 128)), code(E, N, K), one(E, -(-N // 128), -(-K // 128)), _dev(off), y.t)
+        assert y.intact()
+    blocks = m.fp8_ragged_blocks(R, E)
+    s8 = lambda c: torch.full((blocks, c), 127, dtype=torch.uint8, device=DEV)
+    for dt in DT.values():
+        dw = _Guarded((E, N, K), dt)
+        m.grouped_gemm_fp8_wgrad(code(blocks, N, 128), s8(N), code(blocks, K, 128), s8(K), _dev(off), R, dw.t)
+        assert dw.intact()
+    x = _randn((R, K), "bf16", 1).to(DEV)
+    out = [_Guarded((R, K), torch.uint8), _Guarded((-(-K // 128), R), torch.uint8), _Guarded((blocks, K, 128), torch.uint8),
+           _Guarded((blocks, K), torch.uint8)]
+    q, s, qt, ts = (o.t.data_ptr() for o in out)
+    assert m.lib().fp8_quant_ragged(x.data_ptr(), 0, K, _dev(off).data_ptr(), R, E, K, q, K, s, 1, R, qt, ts,
+                                    torch.cuda.current_stream().cuda_stream) == 0
+    torch.cuda.synchronize()
+    assert all(o.intact() for o in out)
