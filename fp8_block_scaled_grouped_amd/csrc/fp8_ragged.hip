@@ -220,9 +220,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_ragged_kernel(Fp8Args g) 
   constexpr int kAhead = TM * TN >= 32 ? 1 : 2, kHold = 2 * kAhead, kHalf = TN / 2;  // fragments of B ahead, and held
   constexpr int kABytes = BM * 128, kHBytes = BN * 64;  // a slot of A, a half of B
   constexpr int NA = kABytes / 1024 / NW, NH = kHBytes / 1024 / NW;  // DMAs of a wave
-  // wgrad's sums are stored past the caches (1.08 ms against 0.99, 32768 rows over 32 experts of 4096 x 7168; 218 us against
-  // 177, 16384 over 32 of 4096 x 2048; fwd's, which the next product reads, 0.81 either way)
-  constexpr int kAux = OP == kFp8Wgrad ? 2 : 0, kBand = OP == kFp8Wgrad ? 4 : 8;
+  // wgrad's sums are stored past the caches (nt and sc1: 0.92 ms, nt alone 0.94, neither 0.95 with 32768 rows over 32 experts of
+  // 4096 x 7168; 551, 566 and 645 us with 16384; fwd's, which the next product reads, 0.81 either way)
+  constexpr int kAux = OP == kFp8Wgrad ? 18 : 0, kBand = OP == kFp8Wgrad ? 4 : 8;
   constexpr int kWinA = (BM + 63) / 64, kWin = kWinA + BN / 64;  // windows of 64 scales: A's rows, then B's columns
   constexpr int kScales = 256 * kWin;                    // scales of a step, a dword each
   static_assert(NA * NW * 1024 == kABytes && NH * NW * 1024 == kHBytes && NW >= kWin && TN >= 4 && TN % 4 == 0, "whole DMAs");

@@ -679,10 +679,18 @@ def _queue(*tensors):
 
 
 def _pairs(row_of_pair):
-    if row_of_pair.dtype != torch.int32 or row_of_pair.dim() != 2 or row_of_pair.shape[1] < 1 or not row_of_pair.is_contiguous():
-        raise ValueError("row_of_pair must be a contiguous int32 tensor [T, topk], got %s %s" % (row_of_pair.dtype,
-                                                                                               tuple(row_of_pair.shape)))
-    return row_of_pair.shape
+    shape = row_of_pair.shape
+    if len(shape) != 2 or shape[1] < 1 or row_of_pair.dtype != torch.int32 or not row_of_pair.is_contiguous():
+        raise ValueError("row_of_pair must be a contiguous int32 tensor [T, topk], got %s %s" % (row_of_pair.dtype, tuple(shape)))
+    return shape
+
+
+def _matrix(t, name):
+    """(rows, columns, row stride) of a 2-D tensor with contiguous rows."""
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError("%s must be 2-D, got %s" % (name, tuple(shape)))
+    return shape[0], shape[1], shape[1] if t.is_contiguous() else _ld(t, name)
 
 
 def _grad_wanted(*tensors):
@@ -708,19 +716,20 @@ def moe_group(topk_ids, E, out=None, workspace=None):
     """
     if topk_ids.dtype != torch.int32:
         raise ValueError("topk_ids must be int32, got %s" % topk_ids.dtype)
-    ld = _ld(topk_ids, "topk_ids")
-    T, k = topk_ids.shape
+    T, k, ld = _matrix(topk_ids, "topk_ids")
+    n = T * k
+    stream = _queue(topk_ids, *out or (), workspace)
     if out is None:
-        offsets, row_of_pair, pair_of_row = topk_ids.new_empty(E + 1), topk_ids.new_empty((T, k)), topk_ids.new_empty(T * k)
+        offsets, row_of_pair, pair_of_row = topk_ids.new_empty(E + 1), topk_ids.new_empty((T, k)), topk_ids.new_empty(n)
     else:
         offsets, row_of_pair, pair_of_row = out
-        for t, shape, name in ((offsets, (E + 1,), "offsets"), (row_of_pair, (T, k), "row_of_pair"), (pair_of_row, (T * k,), "pair_of_row")):
+        for t, shape, name in ((offsets, (E + 1,), "offsets"), (row_of_pair, (T, k), "row_of_pair"), (pair_of_row, (n,), "pair_of_row")):
             _need(t, shape, torch.int32, name)
-    if workspace is None and T * k > 4096:
+    if workspace is None and n > 4096:
         workspace = topk_ids.new_empty(moe_group_workspace(T, k, E), dtype=torch.uint8)
-    stream = _queue(topk_ids, *out or (), workspace)
     ws, wsn = (None, 0) if workspace is None else (_ptr(_dev(workspace, torch.uint8, "workspace")), workspace.numel())
-    _check(lib().moe_group(_ptr(topk_ids), ld, T, k, E, _ptr(offsets), _ptr(row_of_pair), _ptr(pair_of_row), ws, wsn, stream))
+    _check(lib().moe_group(topk_ids.data_ptr(), ld, T, k, E, offsets.data_ptr(), row_of_pair.data_ptr(), pair_of_row.data_ptr(), ws,
+                           wsn, stream))
     return offsets, row_of_pair, pair_of_row
 
 
@@ -742,20 +751,22 @@ def moe_dispatch(x, row_of_pair, rows=None):
     rows [T*topk, H], or any number of rows when given; rows that no pair has are left as they are.  Differentiable for x
     (moe_combine without weights) when rows is not given.
     """
-    if rows is None and _grad_wanted(x):
+    if rows is None and x.requires_grad and torch.is_grad_enabled():
         return _Dispatch.apply(x, row_of_pair)
     dt = _elem(x, "x", 3)
     T, k = _pairs(row_of_pair)
-    if x.dim() != 2 or x.shape[0] != T:
-        raise ValueError("x must be [T, H] with the tokens of row_of_pair")
-    H = x.shape[1]
+    n, H, ld = _matrix(x, "x")
+    if n != T:
+        raise ValueError("x must have the %d tokens of row_of_pair, got %d" % (T, n))
     if rows is None:
-        rows = x.new_empty((T * k, H))
-    elif rows.dim() != 2 or rows.shape[1] != H or rows.dtype != x.dtype:
-        raise ValueError("rows must be [R, %d] in the type of x" % H)
-    stream = _queue(x, row_of_pair, rows)
-    _check(lib().moe_dispatch(_ptr(x), dt, _ld(x, "x"), T, H, k, _ptr(row_of_pair), rows.shape[0], _ptr(rows), _ld(rows, "rows"),
-                              stream))
+        stream = _queue(x, row_of_pair)
+        R, ld_rows, rows = T * k, H, x.new_empty((T * k, H))
+    else:
+        stream = _queue(x, row_of_pair, rows)
+        R, w, ld_rows = _matrix(rows, "rows")
+        if w != H or rows.dtype != x.dtype:
+            raise ValueError("rows must be [R, %d] in the type of x" % H)
+    _check(lib().moe_dispatch(x.data_ptr(), dt, ld, T, H, k, row_of_pair.data_ptr(), R, rows.data_ptr(), ld_rows, stream))
     return rows
 
 
@@ -776,6 +787,8 @@ class _Combine(torch.autograd.Function):
 def _routing_weights(weights, T, k):
     if weights.dtype != torch.float32 or weights.shape != (T, k):
         raise ValueError("weights must be fp32 %s, got %s %s" % ((T, k), weights.dtype, tuple(weights.shape)))
+    if weights.is_contiguous():
+        return k
     return _ld(weights, "weights")
 
 
@@ -789,14 +802,14 @@ def moe_combine(rows, row_of_pair, weights=None, out=None):
         return _Combine.apply(rows, row_of_pair, weights)
     dt = _elem(rows, "rows")
     T, k = _pairs(row_of_pair)
-    if rows.dim() != 2:
-        raise ValueError("rows must be [R, H]")
-    R, H = rows.shape
-    ld_w = 0 if weights is None else _routing_weights(weights, T, k)
-    out = _out(out, (T, H), rows.dtype, rows, "out")
+    R, H, ld = _matrix(rows, "rows")
+    w, ld_w = (None, 0) if weights is None else (weights.data_ptr(), _routing_weights(weights, T, k))
     stream = _queue(rows, row_of_pair, weights, out)
-    _check(lib().moe_combine(_ptr(rows), dt, _ld(rows, "rows"), T, H, k, _ptr(row_of_pair), R, _ptr(weights), ld_w, _ptr(out),
-                             _ld(out, "out"), stream))
+    if out is None:
+        ld_out, out = H, rows.new_empty((T, H))
+    else:
+        ld_out = _ld(_out(out, (T, H), rows.dtype, rows, "out"), "out")
+    _check(lib().moe_combine(rows.data_ptr(), dt, ld, T, H, k, row_of_pair.data_ptr(), R, w, ld_w, out.data_ptr(), ld_out, stream))
     return out
 
 
@@ -808,12 +821,11 @@ def moe_combine_grad(dout, rows, row_of_pair, weights, drows=None, dweights=None
     """
     dt = _elem(rows, "rows")
     T, k = _pairs(row_of_pair)
-    if rows.dim() != 2:
-        raise ValueError("rows must be [R, H]")
-    R, H = rows.shape
+    R, H, ld = _matrix(rows, "rows")
     if dout.shape != (T, H) or dout.dtype != rows.dtype:
         raise ValueError("dout must be %s %s, got %s %s" % (rows.dtype, (T, H), dout.dtype, tuple(dout.shape)))
     ld_w = _routing_weights(weights, T, k)
+    stream = _queue(dout, rows, row_of_pair, weights, drows, dweights)
     drows = _out(drows, (R, H), rows.dtype, rows, "drows") if want[0] else None
     if not want[1]:
         dweights = None
@@ -821,10 +833,9 @@ def moe_combine_grad(dout, rows, row_of_pair, weights, drows=None, dweights=None
         dweights = weights.new_empty((T, k))
     else:
         _need(dweights, (T, k), torch.float32, "dweights")
-    stream = _queue(dout, rows, row_of_pair, weights, drows, dweights)
-    _check(lib().moe_combine_grad(_ptr(dout), _ld(dout, "dout"), _ptr(rows), _ld(rows, "rows"), dt, T, H, k, _ptr(row_of_pair), R,
-                                  _ptr(weights), ld_w, _ptr(drows), 0 if drows is None else _ld(drows, "drows"), _ptr(dweights),
-                                  stream))
+    _check(lib().moe_combine_grad(dout.data_ptr(), _ld(dout, "dout"), rows.data_ptr(), ld, dt, T, H, k, row_of_pair.data_ptr(), R,
+                                  weights.data_ptr(), ld_w, _ptr(drows), 0 if drows is None else _ld(drows, "drows"),
+                                  _ptr(dweights), stream))
     return drows, dweights
 
 
