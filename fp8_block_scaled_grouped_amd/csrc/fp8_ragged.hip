@@ -42,6 +42,7 @@ struct Fp8Args {
   int64_t lda, ldc, ssm, sskb;
   int R, E, N, K;
   int f16;                 // 16-bit outputs: fp16 or bf16
+  int lines;               // wgrad: rows of dw start on lines of 128 bytes
 };
 
 // LDS-DMA of a dword a lane, as dma16_buf.
@@ -148,9 +149,9 @@ __device__ __forceinline__ uint32_t pack16(float a, float b) {
 // c: the wave's first row and column; rows and cols are left from there on (fewer than none: nothing is stored).  Stores past them
 // go past the end of a buffer descriptor, so there is no branch.
 // A store covers 8 rows of 128 bytes: lanes l and l ^ 8 change tiles, and before that, with 16 bits, lanes 16 apart, so that one holds
-// 8 columns, 16 bytes.
-template <bool F16, bool OUT32, int AUX, int TM, int TN>
-__device__ __forceinline__ void store_sums(v4f (&acc)[TM][TN], void* c, int64_t ldc, int rows, int cols, int lane) {
+// 8 columns, 16 bytes.  past (if it MAY be): past the caches.
+template <bool F16, bool OUT32, bool MAY, int TM, int TN>
+__device__ __forceinline__ void store_sums(v4f (&acc)[TM][TN], void* c, int64_t ldc, int rows, int cols, int lane, bool past) {
   constexpr int kSize = OUT32 ? 4 : 2;
   const int r = min(rows, 16 * TM);
   const uint32_t ld = (uint32_t)ldc * kSize;
@@ -170,8 +171,13 @@ __device__ __forceinline__ void store_sums(v4f (&acc)[TM][TN], void* c, int64_t 
     u32x4 first, second;
     halves(p, q, first, second);
     const uint32_t at = n < cols ? (16 * i + (lane & 7)) * ld + n * kSize : kPastEnd;
-    __builtin_amdgcn_raw_buffer_store_b128(first, rsrc, at, 0, AUX);
-    __builtin_amdgcn_raw_buffer_store_b128(second, rsrc, at + 8 * ld, 0, AUX);
+    if (MAY && past) {  // non-temporal
+      __builtin_amdgcn_raw_buffer_store_b128(first, rsrc, at, 0, 2);
+      __builtin_amdgcn_raw_buffer_store_b128(second, rsrc, at + 8 * ld, 0, 2);
+    } else {
+      __builtin_amdgcn_raw_buffer_store_b128(first, rsrc, at, 0, 0);
+      __builtin_amdgcn_raw_buffer_store_b128(second, rsrc, at + 8 * ld, 0, 0);
+    }
   };
   constexpr int kTiles = OUT32 ? 2 : 4;  // 128 bytes
 #pragma unroll
@@ -220,9 +226,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_ragged_kernel(Fp8Args g) 
   constexpr int kAhead = TM * TN >= 32 ? 1 : 2, kHold = 2 * kAhead, kHalf = TN / 2;  // fragments of B ahead, and held
   constexpr int kABytes = BM * 128, kHBytes = BN * 64;  // a slot of A, a half of B
   constexpr int NA = kABytes / 1024 / NW, NH = kHBytes / 1024 / NW;  // DMAs of a wave
-  // wgrad's sums are stored past the caches (nt and sc1: 0.92 ms, nt alone 0.94, neither 0.95 with 32768 rows over 32 experts of
-  // 4096 x 7168; 551, 566 and 645 us with 16384; fwd's, which the next product reads, 0.81 either way)
-  constexpr int kAux = OP == kFp8Wgrad ? 18 : 0, kBand = OP == kFp8Wgrad ? 4 : 8;
+  constexpr int kBand = OP == kFp8Wgrad ? 4 : 8;
   constexpr int kWinA = (BM + 63) / 64, kWin = kWinA + BN / 64;  // windows of 64 scales: A's rows, then B's columns
   constexpr int kScales = 256 * kWin;                    // scales of a step, a dword each
   static_assert(NA * NW * 1024 == kABytes && NH * NW * 1024 == kHBytes && NW >= kWin && TN >= 4 && TN % 4 == 0, "whole DMAs");
@@ -241,11 +245,17 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_ragged_kernel(Fp8Args g) 
     const int mtiles = (g.N + BM - 1) / BM, per = (g.E + kTab - 1) / kTab;
     int* tab = reinterpret_cast<int*>(smem);
     const int total = OP == kFp8Fwd ? fill_table<BM>(g.offsets, g.R, g.E, per, g.R / BM + min(g.E, g.R), tab, lane) * ntiles : g.E * mtiles * ntiles;
-    // each XCD (workgroups go to the eight in turn) takes a run of the tiles, and its workgroups the next one in turn
-    const int chunk = (total + 7) / 8, stride = gridDim.x >> 3;
-    const int first = (int)(blockIdx.x & 7) * chunk + (int)(blockIdx.x >> 3), end = min(total, ((int)(blockIdx.x & 7) + 1) * chunk);
-    if (lane == 0) count_sh = first < end ? min(kMaxTiles, (end - first + stride - 1) / stride) : 0;
-    const int64_t t = first + (int64_t)lane * stride;
+    // Workgroups go to the eight XCDs in turn.  Small tiles: each XCD takes a run of them, and its workgroups the next one in turn
+    // (8192 rows over 32 experts of 2048 x 2048 50 us, else 58).  Large ones, and wgrad's, which cost as much as their
+    // expert has rows: the XCDs take as many as they have workgroups in turn (65536 rows over 32 experts of 4096 x 7168 1.41 ms
+    // against 1.44; wgrad with 32768 rows that follow Zipf's law 0.98 against 2.7).
+    constexpr bool kRuns = OP == kFp8Fwd && BM < 256;
+    const int xcd = blockIdx.x & 7, slot = blockIdx.x >> 3, stride = gridDim.x >> 3;
+    const int64_t chunk = ((int64_t)total + 7) / 8;
+    const int64_t first = xcd * (kRuns ? chunk : (int64_t)stride) + slot, step = kRuns ? stride : 8ll * stride;
+    const int64_t end = kRuns ? min((int64_t)total, (xcd + 1) * chunk) : total;
+    if (lane == 0) count_sh = first < end ? (int)min((int64_t)kMaxTiles, (end - first + step - 1) / step) : 0;
+    const int64_t t = first + lane * step;
     if (t < end) {
       const int q = (int)t / ntiles;
       int e, base, m, lo, hi;
@@ -534,8 +544,13 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_ragged_kernel(Fp8Args g) 
     int l = lane;
     asm volatile("" : "+v"(l));  // the stores' addresses are made here, not kept in registers through the steps
     uint8_t* c = static_cast<uint8_t*>(g.c) + ((row0 + wm) * g.ldc + n0 + wi * (BN / WN)) * (OUT32 ? 4 : 2);
-    if (OUT32 || !g.f16) store_sums<false, OUT32, kAux>(acc, c, g.ldc, mrows - wm, ndim - n0 - wi * (BN / WN), l);
-    else store_sums<true, false, kAux>(acc, c, g.ldc, mrows - wm, ndim - n0 - wi * (BN / WN), l);
+    // wgrad's sums are stored past the caches where rows start on lines (nt: 177 us, else 220, for 16384 rows over 32 experts of
+    // 4096 x 2048), but 25 us become 56 where they do not (5003 over 48 of 1008 x 1168); fwd's are read by the next product
+    const int rows = mrows - wm, cols = ndim - n0 - wi * (BN / WN);
+    const bool past = OP == kFp8Wgrad && g.lines;
+    constexpr bool kMay = OP == kFp8Wgrad;
+    if (OUT32 || !g.f16) store_sums<false, OUT32, kMay>(acc, c, g.ldc, rows, cols, l, past);
+    else store_sums<true, false, kMay>(acc, c, g.ldc, rows, cols, l, past);
   }
   vm_wait<0>();
 }
@@ -613,7 +628,7 @@ extern "C" int grouped_gemm_fp8(const uint8_t* x8, const void* x_scale, int64_t 
   MOE355_CHECK((K == 0 || (aligned16(x8) && ld_x % 16 == 0 && aligned16(w8))) && aligned16(y) && ld_y % 8 == 0 && on4(offsets) &&
                    (e8m0 || (on4(x_scale) && on4(w_scale))),
                MOE355_EMISALIGNED);
-  const Fp8Args g{x8, w8, x_scale, w_scale, y, offsets, ld_x, ld_y, sstride_m, sstride_kb, R, E, N, K, fp16};
+  const Fp8Args g{x8, w8, x_scale, w_scale, y, offsets, ld_x, ld_y, sstride_m, sstride_kb, R, E, N, K, fp16, 0};
   return e8m0 ? run<kFp8Fwd, true, false>(g, stream) : run<kFp8Fwd, false, false>(g, stream);
 }
 
@@ -624,6 +639,7 @@ extern "C" int grouped_gemm_fp8_wgrad(const uint8_t* dyt, const uint8_t* dyt_sca
   if (E == 0 || N == 0 || K == 0) return MOE355_OK;  // without rows every gradient is zero: still written
   MOE355_CHECK(offsets && dw && (R == 0 || (dyt && dyt_scale && xt && xt_scale)), MOE355_EINVAL);
   MOE355_CHECK((R == 0 || (aligned16(dyt) && aligned16(xt))) && aligned16(dw) && on4(offsets), MOE355_EMISALIGNED);
-  const Fp8Args g{dyt, xt, dyt_scale, xt_scale, dw, offsets, 128, K, 0, 0, R, E, N, K, out == MOE355_F16};
+  const int lines = (int64_t)K * (out == MOE355_F32 ? 4 : 2) % 128 == 0 && reinterpret_cast<uintptr_t>(dw) % 128 == 0;
+  const Fp8Args g{dyt, xt, dyt_scale, xt_scale, dw, offsets, 128, K, 0, 0, R, E, N, K, out == MOE355_F16, lines};
   return out == MOE355_F32 ? run<kFp8Wgrad, true, true>(g, stream) : run<kFp8Wgrad, true, false>(g, stream);
 }
