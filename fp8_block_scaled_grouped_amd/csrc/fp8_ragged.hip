@@ -212,26 +212,27 @@ __device__ __forceinline__ void store_sums(v4f (&acc)[TM][TN], void* c, int64_t 
 //
 // The steps of all tiles of a workgroup are one stream: while one tile's last steps are multiplied and its sums are
 // stored, the operands of the next are on their way.  A step's rows j = 0 .. TN - 1 multiply fragment j of B with the TM fragments of A.
-// A(s) is read ahead, during step s - 1; B's fragments are read two rows ahead.  Two barriers a step:
-//   row 1     A(s) is in everyone's registers and B(s - 1) is done with: A(s + 2) and its scales follow into A(s)'s slot
-//   row TN/2  A(s + 1), B(s + 1) and their scales have landed (the DMAs of A(s + 2) may be under way) and the first half of B(s)'s
-//             fragments is done with: B(s + 2) follows, its halves in the slots of the second half of B(s - 1) and the first of B(s)
-// So LDS holds two slots of A and five halves of B, and DMAs go out in every part of a step.  Measured on 65536 rows over 32 experts of
+// A(s) is read ahead, during step s - 1; B's fragments are read one or two rows ahead.  Two barriers a step:
+//   row 1     A(s) is in everyone's registers and B(s - 1) is done with: A(s + D) and its scales follow into A(s)'s slot
+//   row TN/2  A(s + 1), B(s + 1) and their scales have landed (the DMAs of later steps may be under way) and the first half of B(s)'s
+//             fragments is done with: B(s + D) follows, its halves in the slots of the second half of B(s - 1) and the first of B(s)
+// So LDS holds D slots of A and 2 D + 1 halves of B, and DMAs go out in every part of a step.  Measured on 65536 rows over 32 experts of
 // 4096 x 7168, E8M0 (fp32 scales; gradient for w): one barrier a step, all DMAs in its second half and scales loaded into registers
 // 1.80 ms (1.87; 2.15); so 1.48 (1.65; 1.67), most of the last from one tile's start under another's end: with 8 steps a tile (16384 rows
 // over 32 experts of 4096 x 2048) 0.229 ms against 0.320.
-template <int OP, bool E8, bool OUT32, int BM, int BN, int WM, int WN>
+template <int OP, bool E8, bool OUT32, int BM, int BN, int WM, int WN, int D>
 __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_ragged_kernel(Fp8Args g) {
   constexpr int NW = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
   constexpr int kAhead = TM * TN >= 32 ? 1 : 2, kHold = 2 * kAhead, kHalf = TN / 2;  // fragments of B ahead, and held
   constexpr int kABytes = BM * 128, kHBytes = BN * 64;  // a slot of A, a half of B
   constexpr int NA = kABytes / 1024 / NW, NH = kHBytes / 1024 / NW;  // DMAs of a wave
   constexpr int kBand = OP == kFp8Wgrad ? 4 : 8;
+  constexpr int kStage = NA + 1 + 2 * NH;  // DMAs of a wave for a step
   constexpr int kWinA = (BM + 63) / 64, kWin = kWinA + BN / 64;  // windows of 64 scales: A's rows, then B's columns
   constexpr int kScales = 256 * kWin;                    // scales of a step, a dword each
   static_assert(NA * NW * 1024 == kABytes && NH * NW * 1024 == kHBytes && NW >= kWin && TN >= 4 && TN % 4 == 0, "whole DMAs");
-  static_assert(kHalf - 1 >= 1 && NA + 1 < 64, "A's DMAs go out in rows 1 .. TN/2 - 1");
-  __shared__ __align__(16) uint8_t smem[2 * kABytes + 5 * kHBytes + 3 * kScales];
+  static_assert(D >= 2 && kHalf >= 2, "A's DMAs go out in rows 1 .. TN/2 - 1");
+  __shared__ __align__(16) uint8_t smem[D * kABytes + (2 * D + 1) * kHBytes + (D + 1) * kScales];
   __shared__ Tile tiles[kMaxTiles];
   __shared__ int count_sh;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -328,8 +329,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_ragged_kernel(Fp8Args g) 
   int ft = -1, fs = 0, fsteps = 0;  // tile and step of the next operands
   const uint8_t *pa = nullptr, *pb = nullptr, *ps = nullptr;
   int lena = 0, lenb = 0, lens = 0;
-  // E8: where a step's bytes start in their dwords, of A's scales and of B's (this step's, the next one's, the one fetched)
-  uint32_t lowa = 0, lowb = 0, rema[3], remb[3];
+  // E8: where a step's bytes start in their dwords, of A's scales and of B's (this step's, the next one's, .., the one fetched)
+  uint32_t lowa = 0, lowb = 0, rema[D + 1], remb[D + 1];
   // to the next tile that has steps; past the last one nothing is fetched
   auto seek = [&]() __attribute__((always_inline)) {
     fs = 0;
@@ -364,8 +365,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_ragged_kernel(Fp8Args g) 
     srem = E8 ? (uint32_t)(uintptr_t)ps & 3u : 0u;
     ds = dma_buffer(ps - srem, (lens + (int)srem + 3) & ~3);
     ps += of_a ? stepsa : stepsb;
-    rema[2] = lowa;
-    remb[2] = lowb;
+    rema[D] = lowa;
+    remb[D] = lowb;
     lowa += (uint32_t)stepsa;
     lowb += (uint32_t)stepsb;
   };
@@ -375,7 +376,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_ragged_kernel(Fp8Args g) 
     if (OP == kFp8Fwd) lenb -= 128;
     ++fs;
   };
-  const uint32_t lds0 = lds_addr(smem), ldss = lds0 + 2 * kABytes + 5 * kHBytes;
+  const uint32_t lds0 = lds_addr(smem), ldss = lds0 + D * kABytes + (2 * D + 1) * kHBytes;
   auto dma_a = [&](int i, uint32_t slot) { dma16_buf(da, (offa | past) + rowa(i), slot + (w * NA + i) * 1024); };
   auto dma_b = [&](int h, int i, uint32_t slot) { dma16_buf(db, (offb | past) + rowb(h, i), slot + (w * NH + i) * 1024); };
   auto dma_s = [&](uint32_t slot) { dma4_buf(ds, E8 ? (soff + srem) & ~3u : soff, slot + win * 256); };
@@ -391,39 +392,43 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_ragged_kernel(Fp8Args g) 
 #pragma unroll
     for (int j = 0; j < TN; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
 
-  uint32_t hb[5], sl[2] = {lds0, lds0 + kABytes};  // halves of B and slots of A: this step's, the next one's, ..
+  uint32_t sl[D], hb[2 * D + 1], sc[D + 1];  // slots of A, halves of B and scales: this step's, the next one's, ..
 #pragma unroll
-  for (int i = 0; i < 5; ++i) hb[i] = lds0 + 2 * kABytes + i * kHBytes;
-  uint32_t sc = ldss, sn = ldss + kScales, sf = ldss + 2 * kScales;  // scales of this step and of the next two
+  for (int i = 0; i < D; ++i) sl[i] = lds0 + i * kABytes;
+#pragma unroll
+  for (int i = 0; i <= 2 * D; ++i) hb[i] = lds0 + D * kABytes + i * kHBytes;
+#pragma unroll
+  for (int i = 0; i <= D; ++i) sc[i] = ldss + i * kScales;
   vm_wait<0>();
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
+  for (int s = 0; s < D; ++s) {
     if (fs == fsteps) seek();
     next_a();
 #pragma unroll
     for (int i = 0; i < NA; ++i) dma_a(i, sl[s]);
-    dma_s(s ? sn : sc);
-    rema[s] = rema[2];
-    remb[s] = remb[2];
+    dma_s(sc[s]);
+    rema[s] = rema[D];
+    remb[s] = remb[D];
     next_b();
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int i = 0; i < NH; ++i) dma_b(h, i, hb[2 * s + h]);
   }
-  vm_wait<0>();  // both steps: no stores stand behind the second's DMAs yet, as the first wait of a tile takes for granted
+  // two steps: no stores stand behind the second's DMAs yet, as the first wait of a tile takes for granted
+  vm_wait<(D - 2) * kStage>();
   barrier_only();
   v8i ra[2][TM], rb[kHold];
   uint32_t rawa[TM], rawb[kHold];  // scales of A's fragments (this step's, then the next one's) and of B's held ones
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
-    ra[0][i] = read_frag(lds0, ata, i);
-    rawa[i] = read_u32(sc + atsa + 64 * i);
+    ra[0][i] = read_frag(sl[0], ata, i);
+    rawa[i] = read_u32(sc[0] + atsa + 64 * i);
   }
 #pragma unroll
   for (int j = 0; j < kAhead; ++j) {
     rb[j] = read_frag(hb[0], atb, j);
-    rawb[j] = read_u32(sc + atsb + (OP == kFp8Wgrad ? 64 * j : 0));
+    rawb[j] = read_u32(sc[0] + atsb + (OP == kFp8Wgrad ? 64 * j : 0));
   }
 
   // first: of a tile, so the stores of the last one's sums are behind the DMAs that row TN/2 waits for and may be under way
@@ -447,33 +452,33 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_ragged_kernel(Fp8Args g) 
         next_a();
       }
       if (j == kHalf) {
-        vm_wait<NA + 1 + kLate>();
+        vm_wait<NA + 1 + (D - 2) * kStage + kLate>();
         barrier_only();
         next_b();
       }
       const int ahead = j + kAhead;
       rb[ahead % kHold] = read_frag(ahead < TN ? hb[ahead / kHalf] : hb[2], atb, ahead % kHalf);
-      if constexpr (OP == kFp8Wgrad) rawb[ahead % kHold] = read_u32((ahead < TN ? sc : sn) + atsb + 64 * (ahead % TN));
+      if constexpr (OP == kFp8Wgrad) rawb[ahead % kHold] = read_u32(sc[ahead < TN ? 0 : 1] + atsb + 64 * (ahead % TN));
       if (j >= 1 && j < kHalf) {
         constexpr int kRow = (NA + 1 + kHalf - 2) / (kHalf - 1);
 #pragma unroll
         for (int d = (j - 1) * kRow; d < j * kRow; ++d) {
-          if (d < NA) dma_a(d, sl[PAR]);
-          else if (d == NA) dma_s(sf);
+          if (d < NA) dma_a(d, sl[0]);
+          else if (d == NA) dma_s(sc[D]);
         }
       }
       if (j >= kHalf) {
         constexpr int kRow = 2 * NH / kHalf, kReads = (TM + kHalf - 1) / kHalf;
 #pragma unroll
-        for (int d = (j - kHalf) * kRow; d < (j - kHalf + 1) * kRow; ++d) dma_b(d / NH, d % NH, hb[d < NH ? 4 : 0]);
+        for (int d = (j - kHalf) * kRow; d < (j - kHalf + 1) * kRow; ++d) dma_b(d / NH, d % NH, hb[d < NH ? 2 * D : 0]);
 #pragma unroll
         for (int d = (j - kHalf) * kReads; d < (j - kHalf + 1) * kReads && d < TM; ++d) {
-          ra[PAR ^ 1][d] = read_frag(sl[PAR ^ 1], ata, d);
-          rawa[d] = read_u32(sn + atsa + 64 * d);
+          ra[PAR ^ 1][d] = read_frag(sl[1], ata, d);
+          rawa[d] = read_u32(sc[1] + atsa + 64 * d);
         }
       }
       if constexpr (OP == kFp8Fwd) {
-        if (j == TN - 1) rawb[0] = read_u32(sn + atsb);
+        if (j == TN - 1) rawb[0] = read_u32(sc[1] + atsb);
       }
 #pragma unroll
       for (int i = 0; i < TM; ++i) {
@@ -501,19 +506,21 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_ragged_kernel(Fp8Args g) 
     for (int i = 0; i < TM; ++i)
 #pragma unroll
       for (int j = 0; j < TN; ++j) asm volatile("" : "+v"(acc[i][j]));
-    const uint32_t h0 = hb[0], h1 = hb[1], s0 = sc;
-    hb[0] = hb[2];
-    hb[1] = hb[3];
-    hb[2] = hb[4];
-    hb[3] = h0;
-    hb[4] = h1;
-    sc = sn;
-    sn = sf;
-    sf = s0;
-    rema[0] = rema[1];
-    rema[1] = rema[2];
-    remb[0] = remb[1];
-    remb[1] = remb[2];
+    const uint32_t a0 = sl[0], h0 = hb[0], h1 = hb[1], s0 = sc[0];
+#pragma unroll
+    for (int i = 0; i + 1 < D; ++i) sl[i] = sl[i + 1];
+    sl[D - 1] = a0;
+#pragma unroll
+    for (int i = 0; i + 2 <= 2 * D; ++i) hb[i] = hb[i + 2];
+    hb[2 * D - 1] = h0;
+    hb[2 * D] = h1;
+#pragma unroll
+    for (int i = 0; i < D; ++i) {
+      sc[i] = sc[i + 1];
+      rema[i] = rema[i + 1];
+      remb[i] = remb[i + 1];
+    }
+    sc[D] = s0;
   };
   for (int t = 0; t < count; ++t) {
     int left = uniform(tiles[t].steps);
@@ -534,9 +541,6 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_ragged_kernel(Fp8Args g) 
       } else {
 #pragma unroll
         for (int i = 0; i < TM; ++i) ra[0][i] = ra[1][i];
-        const uint32_t was = sl[0];
-        sl[0] = sl[1];
-        sl[1] = was;
       }
     }
     const int64_t row0 = uniform64(tiles[t].row0);
@@ -555,15 +559,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_ragged_kernel(Fp8Args g) 
   vm_wait<0>();
 }
 
-template <int OP, bool E8, bool OUT32, int BM, int BN, int WM, int WN>
+template <int OP, bool E8, bool OUT32, int BM, int BN, int WM, int WN, int D = 2>
 int launch(const Fp8Args& g, hipStream_t stream) {
-  auto* fn = &fp8_ragged_kernel<OP, E8, OUT32, BM, BN, WM, WN>;
+  auto* fn = &fp8_ragged_kernel<OP, E8, OUT32, BM, BN, WM, WN, D>;
   const int64_t nt = ceil_div64(OP == kFp8Fwd ? g.N : g.K, BN);
   // an upper bound of the row tiles: the offsets are on the device
   const int64_t mt = OP == kFp8Wgrad ? (int64_t)g.E * ceil_div64(g.N, BM) : g.R / BM + (g.E < g.R ? g.E : g.R);
   MOE355_CHECK(mt * nt < (1ll << 31), MOE355_EUNSUPPORTED);  // tiles are counted in 32 bits
   // as many workgroups as the CUs hold at a time, or tiles; more where one would get more than kMaxTiles
-  const int64_t slots = 256 * (BM == 256 ? 1 : BN == 128 ? 2 : 4), need = ceil_div64(ceil_div64(mt * nt, 8), kMaxTiles) * 8;
+  const int64_t slots = 256 * (BM == 256 ? 1 : 2), need = ceil_div64(ceil_div64(mt * nt, 8), kMaxTiles) * 8;
   const int64_t few = ceil_div64(mt * nt, 8) * 8 < slots ? ceil_div64(mt * nt, 8) * 8 : slots, grid = few > need ? few : need;
   hipLaunchKernelGGL(fn, dim3((unsigned)grid), dim3(64 * WM * WN), 0, stream, g);
   return launch_status();
@@ -580,13 +584,15 @@ double expected_tiles(int R, int E, int t) {
   return n * E;
 }
 
-// The tile.  Few tiles, or few rows an expert: 32 x 64 by two waves, four workgroups a CU; the weights' bytes bound the latter, and
-// what counts is how many of them are on their way.  From 13 to 40 rows an expert 64 x 128.  Beyond, the cheaper one of
-// 256 x 256, in whole rounds of the 256 CUs, and 128 x 128, whose round of 512 costs 0.715 of that.
-// Measured, us with tiles of 32 x 64 / 64 x 128 / 128 x 128 (fp32 scales):
-//   8 rows over 256 experts of 4096 x 7168 42 / 44 / 45; 512 rows over 256 of 7168 x 2048 538 / 540 / 562;
-//   32 experts of 4096 x 7168: 2 rows each on average 139 / 144 / 153, 8 rows 160 / 160 / 164, 32 rows 220 / 168 / 176,
-//   64 rows 312 / 234 / 198; 300 rows over 4 experts of 512 x 2048 (E8M0) 10.2 / 12.4 / 14.5
+// The tile.  One round of tiles, or few rows an expert: 32 x 64 by two waves, two workgroups a CU with four steps on their way each;
+// the weights' bytes bound the latter, and what counts is how many of them are under way.  From 13 to 40 rows an expert 64 x 128.
+// Beyond, the cheaper one of 256 x 256, in whole rounds of the 256 CUs, and 128 x 128, whose round of 512 costs 0.715 of that.
+// Measured, us with tiles of 32 x 64 / 64 x 128 / 128 x 128, weights out of HBM (fp32 scales; the latter two with two steps ahead):
+//   one row by 4096 x 7168 24 / 28 / 33; 8 rows over 256 experts of 4096 x 7168 43 / 44 / 45; 512 rows over 256 of 7168 x 2048
+//   526 / 540 / 562; 32 experts of 4096 x 7168: 2 rows each on average 139 / 144 / 153, 8 rows 160 / 160 / 164, 32 rows 220 / 168 / 176,
+//   64 rows 312 / 234 / 198; 300 rows over 4 experts of 512 x 2048 (E8M0) 11.0 / 12.6 / 14.4; 600 over 8 of 2048 x 1024, more
+//   than one round, 12.7 / 10.2 / 11.0.  The 32 x 64 with two steps ahead and four workgroups a CU took 41 for the one row and 53 for
+//   the 8; three ahead or six in place of four 44 and more for the 8.
 // and of 128 x 128 / 256 x 256 (E8M0; wgrad in brackets):
 //   32 experts of 2048 x 2048: 128 rows each on average 35 / 33 (82 / 76), 256 rows 50 / 56 (108 / 101); 160 rows of
 //   4096 x 2048 87 / 75 (187 / 162); 2 experts of 2000 x 2000, 500 rows 15 / 26 (12.4 / 14.6); one of 4096 x 7168, 4096 rows
@@ -598,7 +604,7 @@ int run(const Fp8Args& g, hipStream_t stream) {
     return (OP == kFp8Wgrad ? (double)g.E * ceil_div64(g.N, tm) : expected_tiles(g.R, g.E, tm)) * ceil_div64(cols, tn);
   };
   if constexpr (OP == kFp8Fwd) {
-    if (g.R <= 12ll * g.E || tiles(32, 64) <= 1024) return launch<OP, E8, OUT32, 32, 64, 2, 1>(g, stream);
+    if (g.R <= 12ll * g.E || tiles(32, 64) <= 512) return launch<OP, E8, OUT32, 32, 64, 2, 1, 4>(g, stream);
     if (g.R <= 40ll * g.E) return launch<OP, E8, OUT32, 64, 128, 4, 2>(g, stream);
   }
   if (ceil(tiles(256, 256) / 256) <= 0.715 * tiles(128, 128) / 512) return launch<OP, E8, OUT32, 256, 256, 4, 2>(g, stream);
