@@ -9,8 +9,8 @@
 // Bound by memory: 2 bytes in, 1 or 2 out for each value.
 //
 // Scales.  E8M0: byte c stands for 2^(c - 127), the smallest power of two that keeps the block in +-448
-// (448 = 1.75 * 2^8), so nothing saturates and codes are the nearest e4m3 of x * 2^(127 - c), which is
-// exact before its rounding.  A block that holds an infinity or a NaN gets byte 255, NaN.
+// (448 = 1.75 * 2^8), so nothing saturates and codes are the nearest e4m3 of x * 2^(127 - c), rounded
+// once.  A block that holds an infinity or a NaN gets byte 255 and codes of NaN.
 #include "device_common.h"
 #include "frag16.h"
 #include "host_common.h"
@@ -21,6 +21,9 @@ namespace {
 constexpr int kThreads = 256;
 
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+typedef short s16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 b16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 h16x2 __attribute__((ext_vector_type(2)));
 
 __device__ __forceinline__ uint32_t max16x2(uint32_t a, uint32_t b) {
   return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
@@ -40,9 +43,6 @@ __device__ __forceinline__ uint32_t e8m0_of(uint32_t amax16) {
   return (uint32_t)max(0, (int)(u >> 23) - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0));
 }
 
-// 2^(127 - c); 0 for the byte of NaN
-__device__ __forceinline__ float inverse_e8m0(uint32_t c) { return c == 255u ? 0.0f : __uint_as_float((254u - c) << 23); }
-
 // byte b of the result: byte `at` of w[b]
 __device__ __forceinline__ uint32_t gather_bytes(const uint32_t w0, const uint32_t w1, const uint32_t w2, const uint32_t w3,
                                                  int at) {
@@ -55,26 +55,36 @@ struct Tile {
   uint32_t v[8][4];
 };
 
+// Codes of the four values in two words with the scale of E8M0 byte c.  The conversion divides by the power of two and rounds
+// once: for every 16-bit value and byte that keep it in +-448 the same code as the product with 2^(127 - c) rounded by
+// f32x4_to_e4m3, NaN for byte 255 (all 65536 x 256 of either type compared), and one instruction in place of nine a pair.
 template <bool F16>
-__device__ __forceinline__ uint2 codes8(const uint32_t (&v)[4], const float (&m)[8]) {
-  float f[8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = value16<F16>(v[i] & 0xffffu) * m[2 * i];
-    f[2 * i + 1] = value16<F16>(v[i] >> 16) * m[2 * i + 1];
+__device__ __forceinline__ uint32_t codes4(uint32_t lo, uint32_t hi, uint32_t c) {
+  const float s = __uint_as_float(c << 23);
+  s16x2 r = {0, 0};
+  if constexpr (F16) {
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f16(r, __builtin_bit_cast(h16x2, lo), s, false);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f16(r, __builtin_bit_cast(h16x2, hi), s, true);
+  } else {
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(b16x2, lo), s, false);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(b16x2, hi), s, true);
   }
-  return make_uint2(f32x4_to_e4m3(f[0], f[1], f[2], f[3]), f32x4_to_e4m3(f[4], f[5], f[6], f[7]));
+  return __builtin_bit_cast(uint32_t, r);
 }
 
-// Row-major codes q[8 rows][8 columns of this thread] -> LDS tile [128 columns][128 rows].  A column's 16-byte
+// Codes of 8 rows of a column -> LDS tile [128 columns][128 rows], i of the thread's columns.  A column's 16-byte
 // chunk c stands in slot c ^ (column / 8 % 8).
+__device__ __forceinline__ void put_column(uint8_t* lds, uint2 col, int i, int cg, int rg) {
+  *reinterpret_cast<uint2*>(lds + (8 * cg + i) * 128 + (((rg >> 1) ^ (cg & 7)) << 4) + 8 * (rg & 1)) = col;
+}
+// Row-major codes q[8 rows][8 columns of this thread] into that tile
 __device__ __forceinline__ void put_transposed(uint8_t* lds, const uint2 (&q)[8], int cg, int rg) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     auto word = [&](int r) { return i < 4 ? q[r].x : q[r].y; };
     const uint2 col = make_uint2(gather_bytes(word(0), word(1), word(2), word(3), i & 3),
                                  gather_bytes(word(4), word(5), word(6), word(7), i & 3));
-    *reinterpret_cast<uint2*>(lds + (8 * cg + i) * 128 + (((rg >> 1) ^ (cg & 7)) << 4) + 8 * (rg & 1)) = col;
+    put_column(lds, col, i, cg, rg);
   }
 }
 // chunk c of a column of that tile
@@ -82,20 +92,30 @@ __device__ __forceinline__ u32x4 get_transposed(const uint8_t* lds, int col, int
   return *reinterpret_cast<const u32x4*>(lds + col * 128 + ((c ^ ((col >> 3) & 7)) << 4));
 }
 
+// the largest halves of 16 lanes side by side, to all of them
+__device__ __forceinline__ uint32_t max16x2_row(uint32_t m) {
+  m = max16x2(m, __builtin_amdgcn_update_dpp(0, m, 0xb1, 0xf, 0xf, true));   // lanes ^ 1
+  m = max16x2(m, __builtin_amdgcn_update_dpp(0, m, 0x4e, 0xf, 0xf, true));   // lanes ^ 2
+  m = max16x2(m, __builtin_amdgcn_update_dpp(0, m, 0x141, 0xf, 0xf, true));  // 7 - lane in each 8
+  return max16x2(m, __builtin_amdgcn_update_dpp(0, m, 0x140, 0xf, 0xf, true));  // 15 - lane
+}
+
 // Block b of 128 rows: expert e's are [off_e / 128 + e, ..), counted from the segment's first row.  Returns
 // the rows [r0, r1) of b, none for the indices that no expert has.
 __device__ __forceinline__ void block_rows(const int32_t* offsets, int R, int E, int b, int lane, int& r0, int& r1) {
-  int before = 0;  // experts whose first block is b or an earlier one
+  int before = 0, lo = 0, hi = 0;  // experts whose first block is b or an earlier one; rows of the last such expert
   for (int e0 = 0; e0 < E; e0 += 64) {
     const int e = e0 + lane;
-    int lo = 0, hi = 0;
-    if (e < E) segment(offsets, R, e, lo, hi);
-    before += __popcll(__ballot(e < E && lo / 128 + e <= b));
+    int l = 0, h = 0;
+    if (e < E) segment(offsets, R, e, l, h);
+    const int n = __popcll(__ballot(e < E && l / 128 + e <= b));
+    if (n == 0) break;
+    before += n;
+    lo = __builtin_amdgcn_readlane(l, n - 1);
+    hi = __builtin_amdgcn_readlane(h, n - 1);
   }
   r0 = r1 = 0;
   if (before == 0) return;
-  int lo, hi;
-  segment(offsets, R, before - 1, lo, hi);
   const int64_t first = lo + (int64_t)max(0, b - (lo / 128 + before - 1)) * 128;
   r0 = (int)min((int64_t)hi, first);
   r1 = (int)min((int64_t)hi, first + 128);
@@ -141,14 +161,13 @@ __global__ __launch_bounds__(kThreads) void quant_ragged_kernel(RaggedPackArgs g
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       uint32_t m = max16x2(max16x2(t.v[i][0] & kAbs, t.v[i][1] & kAbs), max16x2(t.v[i][2] & kAbs, t.v[i][3] & kAbs));
-#pragma unroll
-      for (int o = 1; o < 16; o <<= 1) m = max16x2(m, __shfl_xor(m, o, 64));
+      m = max16x2_row(m);
       const uint32_t s = e8m0_of<F16>(max(m & 0xffffu, m >> 16));
-      const float f = inverse_e8m0(s);
-      const float m8[8] = {f, f, f, f, f, f, f, f};
       const int r = r0 + 8 * rg + i;
       if (r < r1) {
-        if (in) *reinterpret_cast<uint2*>(g.q + r * g.ld_q + c) = codes8<F16>(t.v[i], m8);
+        if (in)
+          *reinterpret_cast<uint2*>(g.q + r * g.ld_q + c) =
+              make_uint2(codes4<F16>(t.v[i][0], t.v[i][1], s), codes4<F16>(t.v[i][2], t.v[i][3], s));
         if (cg == 0) g.scale[r * g.ssm + (c0 >> 7) * g.sskb] = (uint8_t)s;
       }
     }
@@ -166,20 +185,18 @@ __global__ __launch_bounds__(kThreads) void quant_ragged_kernel(RaggedPackArgs g
       if ((tid & 63) < 16) cmax[w][4 * cg + j] = m[j];
     }
     __syncthreads();
-    float f[8];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const uint32_t a = max16x2(max16x2(cmax[0][4 * cg + j], cmax[1][4 * cg + j]),
                                  max16x2(cmax[2][4 * cg + j], cmax[3][4 * cg + j]));
-      const uint32_t s0 = e8m0_of<F16>(a & 0xffffu), s1 = e8m0_of<F16>(a >> 16);
-      f[2 * j] = inverse_e8m0(s0);
-      f[2 * j + 1] = inverse_e8m0(s1);
-      if (rg == 0 && in) *reinterpret_cast<uint16_t*>(g.tscale + (int64_t)b * g.C + c + 2 * j) = (uint16_t)(s0 | s1 << 8);
-    }
-    uint2 q[8];
+      const uint32_t s[2] = {e8m0_of<F16>(a & 0xffffu), e8m0_of<F16>(a >> 16)};
+      if (rg == 0 && in) *reinterpret_cast<uint16_t*>(g.tscale + (int64_t)b * g.C + c + 2 * j) = (uint16_t)(s[0] | s[1] << 8);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = codes8<F16>(t.v[i], f);
-    put_transposed(lds, q, cg, rg);
+      for (int h = 0; h < 2; ++h) {
+        auto pair = [&](int r) { return __builtin_amdgcn_perm(t.v[r + 1][j], t.v[r][j], h ? 0x07060302u : 0x05040100u); };
+        put_column(lds, make_uint2(codes4<F16>(pair(0), pair(2), s[h]), codes4<F16>(pair(4), pair(6), s[h])), 2 * j + h, cg, rg);
+      }
+    }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -231,10 +248,8 @@ __global__ __launch_bounds__(kThreads) void quant_weight_kernel(WeightPackArgs g
   uint2 q[8];
   if constexpr (E8) {
     const uint32_t s = e8m0_of<F16>(m);
-    const float f = inverse_e8m0(s);
-    const float m8[8] = {f, f, f, f, f, f, f, f};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = codes8<F16>(t.v[i], m8);
+    for (int i = 0; i < 8; ++i) q[i] = make_uint2(codes4<F16>(t.v[i][0], t.v[i][1], s), codes4<F16>(t.v[i][2], t.v[i][3], s));
     if (tid == 0) {
       static_cast<uint8_t*>(g.scale)[at] = (uint8_t)s;
       if (g.qt) static_cast<uint8_t*>(g.tscale)[tat] = (uint8_t)s;
