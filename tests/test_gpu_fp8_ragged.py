@@ -98,6 +98,34 @@ def test_quant_ragged(m, counts, lead, tail, K, dtype):
     assert (q2.cpu().numpy() == rq).all() and (s2.cpu().numpy() == rs).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_quant_every_value_under_every_scale(m, dtype):
+    """Blocks of 127 values under each largest magnitude 448 * 2^e: every value of the 21 binades below it, so subnormal codes,
+    all ties and those that round to zero."""
+    bits = torch.arange(0, 0x7f80 if dtype == "bf16" else 0x7c00, dtype=torch.int32).to(torch.int16)
+    mags = bits.view(DT[dtype]).double()
+    rows = []
+    for e in range(-126, 120) if dtype == "bf16" else range(-23, 8):
+        top = torch.tensor(448.0 * 2.0 ** e, dtype=torch.float64)
+        some = mags[(mags <= top) & (mags >= top * 2.0 ** -21)]
+        some = torch.cat([some, -some])
+        some = torch.nn.functional.pad(some, (0, -some.numel() % 127)).view(-1, 127)
+        rows.append(torch.cat([top.expand(some.shape[0], 1), some], 1))
+    x64 = torch.cat(rows)
+    x = x64.to(DT[dtype])
+    assert torch.equal(x.double(), x64)
+    rq, rs = o.quant_blocks(x64.numpy(), 1)
+    q, s, _, _ = m.fp8_quant_ragged(x.to(DEV), columns=False)
+    assert (s.cpu().numpy() == rs).all() and (q.cpu().numpy() == rq).all()
+    xt = x.t()[:, :x.shape[0] // 8 * 8].contiguous()                   # the same blocks as columns of 128 rows
+    _, _, qt, ts = m.fp8_quant_ragged(xt.to(DEV), _dev([0, 128]), rows=False)
+    n = xt.shape[1]
+    assert (ts[0].cpu().numpy() == rs[:n, 0]).all() and (qt[0].cpu().numpy() == rq[:n]).all()
+    wq, ws = m.fp8_quant_128x128(x[:128].to(DEV)[None])
+    rwq, rws = o.quant_blocks(x64.numpy()[:128], 128)
+    assert (wq[0].cpu().numpy() == rwq).all() and (ws[0].cpu().numpy() == rws).all()
+
+
 def test_quant_ragged_strided_rows(m):
     x = _randn((150, 400), "bf16", 1).to(DEV)
     off = _dev([0, 20, 150])
