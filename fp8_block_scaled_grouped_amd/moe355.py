@@ -773,14 +773,21 @@ def moe_dispatch(x, row_of_pair, rows=None):
 class _Combine(torch.autograd.Function):
     @staticmethod
     def forward(ctx, rows, row_of_pair, weights):
-        ctx.save_for_backward(rows, row_of_pair, weights)
+        ctx.rows = rows.shape[0]
+        ctx.save_for_backward(row_of_pair, *(() if weights is None else (weights, rows)))
         return moe_combine(rows, row_of_pair, weights)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dout):
-        rows, row_of_pair, weights = ctx.saved_tensors
-        drows, dw = moe_combine_grad(dout.contiguous(), rows, row_of_pair, weights, want=ctx.needs_input_grad[0::2])
+        row_of_pair, *rest = ctx.saved_tensors
+        dout = dout.contiguous()
+        # rows that no pair has get a gradient of zeros
+        drows = dout.new_zeros((ctx.rows, dout.shape[1])) if ctx.needs_input_grad[0] else None
+        if not rest:
+            return moe_dispatch(dout, row_of_pair, drows), None, None
+        weights, rows = rest
+        drows, dw = moe_combine_grad(dout, rows, row_of_pair, weights, drows, want=ctx.needs_input_grad[0::2])
         return drows, None, dw
 
 
@@ -796,9 +803,9 @@ def moe_combine(rows, row_of_pair, weights=None, out=None):
     """Rows [R, H] (bf16, fp16 or fp32) back to tokens: out[t] = sum over j of weights[t, j] * rows[row_of_pair[t, j]],
     [T, H] in the type of rows; fp32 sums over ascending j.  weights fp32 [T, topk], None for ones.
 
-    Differentiable for rows and weights when weights are given and out is not.
+    Differentiable for rows and weights when out is not given; rows that no pair has get gradients of zeros.
     """
-    if out is None and weights is not None and _grad_wanted(rows, weights):
+    if out is None and _grad_wanted(rows, weights):
         return _Combine.apply(rows, row_of_pair, weights)
     dt = _elem(rows, "rows")
     T, k = _pairs(row_of_pair)
@@ -981,7 +988,8 @@ def grouped_linear_fp8(x, w, offsets):
     scale for each block (x 1 x 128, w 128 x 128) and multiplied, and so are the gradients: dx from dy in 1 x 128 and
     the same w, dw from dy and x in blocks of 128 rows x 1.  What the backward pass keeps is x and w in 8 bits.
 
-    N and K multiples of 16.  Every row of x must lie in a segment: rows in none have no defined output or gradient.
+    N and K multiples of 16.  Rows of x in no segment have no defined output or gradient (moe_combine and the gradient of
+    moe_dispatch do not read such rows).
     """
     if x.dtype != w.dtype:
         raise ValueError("x and w must have the same type, got %s and %s" % (x.dtype, w.dtype))

@@ -229,6 +229,19 @@ def test_gradients_through_autograd(m):
         assert not m.moe_dispatch(x, drop).requires_grad
 
 
+@pytest.mark.parametrize("weighted", [False, True])
+def test_gradient_of_rows_that_no_pair_has_is_zero(m, weighted):
+    rows = _randn((6, 32), "fp32", 1).to(DEV).requires_grad_()
+    rop = torch.tensor([[4, -1], [1, 9]], dtype=torch.int32, device=DEV)
+    w = torch.tensor([[2.0, 3.0], [4.0, 5.0]], device=DEV) if weighted else None
+    g = _randn((2, 32), "fp32", 2).to(DEV)
+    torch.full((6, 32), float("nan"), device=DEV)                        # what a new buffer may hold
+    (d,) = torch.autograd.grad(m.moe_combine(rows, rop, w), rows, g)
+    ref = torch.zeros_like(rows)
+    ref[4], ref[1] = g[0] * (2 if weighted else 1), g[1] * (4 if weighted else 1)
+    assert torch.equal(d, ref)
+
+
 def test_rows_past_two_to_the_31_bytes(m):
     """Row offsets are 64 bits: the last rows of a buffer of 4.3 GB, in it and back."""
     T, k, H = 4, 2, 1 << 15
