@@ -145,7 +145,7 @@ __device__ __forceinline__ uint32_t pack16(float a, float b) {
   else return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b});
 }
 
-// Stores a wave's sums and clears them: lane l holds of tile (i, j) the row 16 i + l % 16 and the four columns from 16 j + 4 (l / 16).
+// Stores a wave's sums: lane l holds of tile (i, j) the row 16 i + l % 16 and the four columns from 16 j + 4 (l / 16).
 // c: the wave's first row and column; rows and cols are left from there on (fewer than none: nothing is stored).  Stores past them
 // go past the end of a buffer descriptor, so there is no branch.
 // A store covers 8 rows of 128 bytes: lanes l and l ^ 8 change tiles, and before that, with 16 bits, lanes 16 apart, so that one holds
@@ -162,9 +162,8 @@ __device__ __forceinline__ void store_sums(v4f (&acc)[TM][TN], void* c, int64_t 
   auto halves = [&](const u32x4& p, const u32x4& q, u32x4& first, u32x4& second) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const uint32_t y = __builtin_amdgcn_update_dpp(0, up ? p[k] : q[k], 0x128, 0xf, 0xf, true);
-      first[k] = up ? y : p[k];
-      second[k] = up ? q[k] : y;
+      first[k] = __builtin_amdgcn_update_dpp(p[k], q[k], 0x128, 0xf, 0xc, false);  // lanes 8 .. 15 of each 16 change
+      second[k] = __builtin_amdgcn_update_dpp(q[k], p[k], 0x128, 0xf, 0x3, false);
     }
   };
   auto store = [&](const u32x4& p, const u32x4& q, int i, int n) {  // columns n of rows 16 i ..
@@ -198,10 +197,12 @@ __device__ __forceinline__ void store_sums(v4f (&acc)[TM][TN], void* c, int64_t 
         }
         store(v[0], v[1], i, 16 * (j + (up ? 2 : 0) + ((lane >> 4) & 1)) + 8 * (lane >> 5));
       }
+      if constexpr (OUT32) {  // cleared one by one: else the compiler keeps what was stored as well
 #pragma unroll
-      for (int k = 0; k < kTiles; ++k) {
-        acc[i][j + k] = v4f{0.f, 0.f, 0.f, 0.f};
-        if constexpr (OUT32) asm volatile("" : "+v"(acc[i][j + k]));  // else the compiler keeps what was stored as well
+        for (int k = 0; k < kTiles; ++k) {
+          acc[i][j + k] = v4f{0.f, 0.f, 0.f, 0.f};
+          asm volatile("" : "+v"(acc[i][j + k]));
+        }
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -431,9 +432,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_ragged_kernel(Fp8Args g) 
     rawb[j] = read_u32(sc[0] + atsb + (OP == kFp8Wgrad ? 64 * j : 0));
   }
 
-  // first: of a tile, so the stores of the last one's sums are behind the DMAs that row TN/2 waits for and may be under way
+  // first: of a tile, so the sums start from zero, and the stores of the last one's are behind the DMAs that row TN/2 waits for and may
+  // be under way
   auto step = [&](auto par_c, auto first_c) __attribute__((always_inline)) {
-    constexpr int PAR = decltype(par_c)::value, kLate = decltype(first_c)::value ? TM * TN / (OUT32 ? 2 : 4) * 2 : 0;
+    constexpr bool kFirst = decltype(first_c)::value, kZero = kFirst && !OUT32;
+    constexpr int PAR = decltype(par_c)::value, kLate = kFirst ? TM * TN / (OUT32 ? 2 : 4) * 2 : 0;
+    const v4f zero{0.f, 0.f, 0.f, 0.f};
     // a byte's place in its dword is the same for all of a lane's rows (16 apart), and for its columns
     const uint32_t sha = E8 ? 8 * ((mod_a + rema[0]) & 3) : 0, shb = E8 ? 8 * ((mod_b + remb[0]) & 3) : 0;
     uint32_t sa[TM];
@@ -445,6 +449,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_ragged_kernel(Fp8Args g) 
     }
     const uint32_t sbu = rawb[0] >> shb;  // fwd: one for all of the wave's columns
     v4f acc2[3];
+    auto fold = [&](int p) __attribute__((always_inline)) {
+      v4f& sum = acc[p % TM][p / TM];
+      sum = kZero ? acc2[p % 3] * f[p % TM] : sum + acc2[p % 3] * f[p % TM];
+    };
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
       if (j == 1) {
@@ -483,14 +491,14 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_ragged_kernel(Fp8Args g) 
 #pragma unroll
       for (int i = 0; i < TM; ++i) {
         if constexpr (E8) {
-          acc[i][j] = mfma_scaled(rb[j % kHold], ra[PAR][i], acc[i][j], OP == kFp8Wgrad ? rawb[j % kHold] >> shb : sbu, sa[i]);
+          acc[i][j] = mfma_scaled(rb[j % kHold], ra[PAR][i], kZero ? zero : acc[i][j], OP == kFp8Wgrad ? rawb[j % kHold] >> shb : sbu, sa[i]);
         } else {
           // the fold of the tile before the last follows each MFMA
           const int q = j * TM + i;
-          acc2[q % 3] = mfma16x16x128_fp8(rb[j % kHold], ra[PAR][i], v4f{0.f, 0.f, 0.f, 0.f});
+          acc2[q % 3] = mfma16x16x128_fp8(rb[j % kHold], ra[PAR][i], zero);
           if (q >= 2) {
             const int p = q - 2;
-            acc[p % TM][p / TM] += acc2[p % 3] * f[p % TM];
+            fold(p);
           }
           __builtin_amdgcn_sched_barrier(0);
         }
@@ -499,7 +507,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_ragged_kernel(Fp8Args g) 
     }
     if constexpr (!E8) {
 #pragma unroll
-      for (int p = TM * TN - 2; p < TM * TN; ++p) acc[p % TM][p / TM] += acc2[p % 3] * f[p % TM];
+      for (int p = TM * TN - 2; p < TM * TN; ++p) fold(p);
     }
     // the sums stay in this step's block: products are not moved past the branches between steps
 #pragma unroll
@@ -542,6 +550,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_ragged_kernel(Fp8Args g) 
 #pragma unroll
         for (int i = 0; i < TM; ++i) ra[0][i] = ra[1][i];
       }
+    } else if (!OUT32) {
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
     }
     const int64_t row0 = uniform64(tiles[t].row0);
     const int mrows = uniform(tiles[t].mrows), n0 = uniform(tiles[t].n0);
