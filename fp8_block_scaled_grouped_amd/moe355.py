@@ -959,27 +959,69 @@ def grouped_gemm_fp8_wgrad(dyt, dyt_scale, xt, xt_scale, offsets, R, dw=None, ou
     return dw
 
 
+def _addresses(buf, sizes):
+    """Addresses of places of these bytes, one after the other on 256 bytes, None for a size of None."""
+    at, out = buf.data_ptr(), []
+    for n in sizes:
+        out.append(None if n is None else at)
+        at += -(-(n or 0) // 256) * 256
+    return out
+
+
+def _places(like, sizes):
+    """A new buffer on `like`'s device for operands of these bytes (each allocation costs the host 1.5 us), and their addresses."""
+    buf = like.new_empty(sum(-(-(n or 0) // 256) * 256 for n in sizes), dtype=torch.uint8)
+    return buf, _addresses(buf, sizes)
+
+
 class _GroupedLinearFp8(torch.autograd.Function):
+    """fp8_quant_ragged, fp8_quant_128x128, grouped_gemm_fp8 and grouped_gemm_fp8_wgrad on the parts of few buffers."""
+
     @staticmethod
     def forward(ctx, x, w, offsets):
         need_x, need_w = ctx.needs_input_grad[:2]
-        q, scale, qt, tscale = fp8_quant_ragged(x, offsets, columns=need_w)
-        packed = fp8_quant_128x128(w, transposed=need_x)
-        ctx.save_for_backward(offsets, qt, tscale, *packed[2:])
-        ctx.w_dtype, ctx.x_dtype = w.dtype, x.dtype
-        return grouped_gemm_fp8(q, scale, *packed[:2], offsets, out_dtype=x.dtype)
+        f16 = _half(x, "x")
+        R, K, ld = _matrix(x, "x")
+        if w.dim() != 3 or w.shape[2] != K or not w.is_contiguous():
+            raise ValueError("w must be a contiguous [E, N, %d] tensor, got %s" % (K, tuple(w.shape)))
+        E, N, _ = w.shape
+        if offsets.dtype != torch.int32 or offsets.shape != (E + 1,) or not offsets.is_contiguous():
+            raise ValueError("offsets must be a contiguous int32 tensor of %d, got %s %s" % (E + 1, offsets.dtype, tuple(offsets.shape)))
+        stream, off, call = _queue(x, w, offsets), offsets.data_ptr(), lib()
+        blocks, NB, KB = R // 128 + E, _nblk(N), _nblk(K)
+        # x and w transposed, for the gradients of w and x
+        ctx.kept = (blocks * K * 128, blocks * K) if need_w else (None, None)
+        ctx.kept += (E * K * N, E * KB * NB) if need_x else (None, None)
+        kept, (qt, ts, wt, wts) = _places(x, ctx.kept)
+        rest, (q, s, wq, ws) = _places(x, (R * K, KB * R, E * N * K, E * NB * KB))
+        y = x.new_empty((R, N))
+        _check(call.fp8_quant_ragged(x.data_ptr(), f16, ld, off, R, E, K, q, K, s, 1, R, qt, ts, stream))
+        _check(call.fp8_quant_128x128(w.data_ptr(), f16, E, N, K, wq, ws, wt, wts, 1, stream))
+        _check(call.grouped_gemm_fp8(q, s, K, 1, R, wq, ws, 1, off, R, E, N, K, y.data_ptr(), N, f16, stream))
+        ctx.save_for_backward(offsets, kept)
+        ctx.sizes = R, E, N, K
+        return y
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
-        offsets, qt, tscale, *wt = ctx.saved_tensors
-        need_x, need_w = ctx.needs_input_grad[:2]
+        offsets, kept = ctx.saved_tensors
+        qt, ts, wt, wts = _addresses(kept, ctx.kept)
+        R, E, N, K = ctx.sizes
         dy = dy.contiguous()
         if dy.data_ptr() % 16:  # a view into a larger gradient may start anywhere
             dy = dy.clone()
-        q, scale, dyt, dyts = fp8_quant_ragged(dy, offsets, rows=need_x, columns=need_w)
-        dx = grouped_gemm_fp8(q, scale, *wt, offsets, out_dtype=ctx.x_dtype) if need_x else None
-        dw = grouped_gemm_fp8_wgrad(dyt, dyts, qt, tscale, offsets, dy.shape[0], out_dtype=ctx.w_dtype) if need_w else None
+        f16, stream, off, call = _half(dy, "dy"), _queue(dy, kept), offsets.data_ptr(), lib()
+        blocks, dx, dw = R // 128 + E, None, None
+        rest, (q, s, dyt, dys) = _places(dy, ((None, None) if wt is None else (R * N, _nblk(N) * R)) +
+                                         ((None, None) if qt is None else (blocks * N * 128, blocks * N)))
+        _check(call.fp8_quant_ragged(dy.data_ptr(), f16, N, off, R, E, N, q, N, s, 1, R, dyt, dys, stream))
+        if wt is not None:
+            dx = dy.new_empty((R, K))
+            _check(call.grouped_gemm_fp8(q, s, N, 1, R, wt, wts, 1, off, R, E, K, N, dx.data_ptr(), K, f16, stream))
+        if qt is not None:
+            dw = dy.new_empty((E, N, K))
+            _check(call.grouped_gemm_fp8_wgrad(dyt, dys, qt, ts, off, R, E, N, K, dw.data_ptr(), f16, stream))
         return dx, dw, None
 
 
