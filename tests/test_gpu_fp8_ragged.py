@@ -432,6 +432,70 @@ def test_linear_and_its_gradients(m, counts, E, N, K, dtype):
     assert torch.equal(s, torch.autograd.grad(y, xd, torch.ones_like(y))[0])
 
 
+def test_linear_without_rows_with_strided_rows_and_twice(m):
+    E, N, K = 3, 48, 32
+    w = _randn((E, N, K), "bf16", 1).to(DEV).requires_grad_()
+    x = torch.zeros((0, K), dtype=torch.bfloat16, device=DEV, requires_grad=True)
+    y = m.grouped_linear_fp8(x, w, _dev([0, 0, 0, 0]))
+    dx, dw = torch.autograd.grad(y, (x, w), torch.zeros_like(y))
+    assert y.shape == (0, N) and dx.shape == (0, K) and dw.shape == w.shape and (dw == 0).all()
+    # rows with a stride, rows in no segment (their outputs and gradients are anything), and a graph that is run twice
+    wide, dy, off = _randn((70, 64), "bf16", 2).to(DEV), _randn((70, N), "bf16", 3).to(DEV), _dev([10, 10, 40, 60])
+    a, b = wide[:, 16:48].requires_grad_(), wide[:, 16:48].detach().contiguous().requires_grad_()
+    ya, yb = m.grouped_linear_fp8(a, w, off), m.grouped_linear_fp8(b, w, off)
+    ga = torch.autograd.grad(ya, (a, w), dy, retain_graph=True)
+    twice, gb = torch.autograd.grad(ya, (a, w), dy), torch.autograd.grad(yb, (b, w), dy)
+    assert torch.equal(ya[10:60], yb[10:60])
+    for g in (twice, gb):
+        assert torch.equal(ga[0][10:60], g[0][10:60]) and torch.equal(ga[1], g[1])
+    # no experts: no row has a segment
+    none = m.grouped_linear_fp8(b.detach(), torch.zeros((0, N, K), dtype=torch.bfloat16, device=DEV), _dev([0]))
+    assert none.shape == (70, N)
+    for bad in (lambda: m.grouped_linear_fp8(b, w[:, :, :16], off), lambda: m.grouped_linear_fp8(b, w.transpose(1, 2), off),
+                lambda: m.grouped_linear_fp8(b, w, off[:2]), lambda: m.grouped_linear_fp8(b, w, off.long()),
+                lambda: m.grouped_linear_fp8(b[None], w, off), lambda: m.grouped_linear_fp8(b.float(), w.float(), off),
+                lambda: m.grouped_linear_fp8(b, w[:, ::2], off)):
+        with pytest.raises(ValueError):
+            bad()
+    odd = torch.zeros((2, 40, K), dtype=torch.bfloat16, device=DEV)       # N no multiple of 16: the gradient for x has no codes
+    with pytest.raises(m.Moe355Error):
+        m.grouped_linear_fp8(b, odd, _dev([0, 10, 70]))
+
+
+def test_linear_and_gradients_captured(m):
+    """Forward and backward in one graph, on leaves made for each run."""
+    E, N, K, R = 4, 144, 272, 300
+    x, dy, w = (torch.empty(s, dtype=torch.bfloat16, device=DEV) for s in ((R, K), (R, N), (E, N, K)))
+    off = torch.empty(E + 1, dtype=torch.int32, device=DEV)
+
+    def step():
+        a, b = x.detach().requires_grad_(), w.detach().requires_grad_()
+        y = m.grouped_linear_fp8(a, b, off)
+        return (y.detach(),) + torch.autograd.grad(y, (a, b), dy)
+
+    def fill(i, counts):
+        x.copy_(_randn((R, K), "bf16", i))
+        dy.copy_(_randn((R, N), "bf16", i + 9))
+        w.copy_(_randn((E, N, K), "bf16", i + 20, 0.05))
+        off.copy_(_dev(_offsets(counts)))
+
+    fill(0, [100, 30, 0, 170])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step()
+    for i, counts in ((1, [0, 150, 150, 0]), (2, [300, 0, 0, 0]), (3, [1, 128, 129, 42])):
+        fill(i, counts)
+        g.replay()
+        torch.cuda.synchronize()
+        again = [t.clone() for t in got]
+        assert all(torch.equal(p, q) for p, q in zip(again, step()))
+
+
 def test_gradients_against_differences(m):
     """On values that quantisation leaves alone the loss is linear in x and in w, so a difference along any direction
     of such values is the gradient.  All is whole numbers: x + u and w + u up to 4, |y| <= 4 * 2 * 16, |dx| <= 2 * 2 * 32 and
