@@ -20,8 +20,8 @@
 // What bounds it: the clock that the card's power leaves, 1.6 GHz under this load, at which the matrix unit is busy 71% of the time
 // (62% with fp32 scales, whose folds are four VALU instructions an MFMA).  A 256 x 256 step brings 64 KB of operands into LDS for 16.8 MFLOP
 // and its waves read 192 KB of fragments back; of an earlier form's 1.48 ms (below) 1.20 remained without the DMAs and 1.49 without
-// the MFMAs.  65536 rows over 32 experts of 4096 x 7168: 1.42 ms (2710 TFLOP/s) with power-of-two scales, 1.57
-// (2460) with fp32 ones, the gradient for w 1.55 (bf16; 1.90 in fp32, 3.8 GB of it); a library product of 8192^3 without block scales runs at
+// the MFMAs.  65536 rows over 32 experts of 4096 x 7168: 1.42 to 1.46 ms (2640 to 2710 TFLOP/s) with power-of-two scales, 1.57
+// (2460) with fp32 ones, the gradient for w 1.55 to 1.57 (bf16; 1.90 in fp32, 3.8 GB of it); a library product of 8192^3 without block scales runs at
 // 2960 to 3000.  Few rows: the weights' bytes, 512 rows over 256 experts of 7168 x 2048 525 us (6.2 TB/s).
 #include <math.h>
 
@@ -226,7 +226,8 @@ __device__ __forceinline__ void store_sums(v4f (&acc)[TM][TN], void* c, int64_t 
 // 4096 x 7168, E8M0 (fp32 scales; gradient for w): one barrier a step, all DMAs in its second half and scales loaded into registers
 // 1.80 ms (1.87; 2.15); so 1.42 (1.57; 1.55), much of the last from one tile's start under another's end: the gradient with 4 steps a tile
 // (16384 rows over 32 experts of 4096 x 2048) 0.166 ms against 0.320.  Of its time with 8 steps a tile (32768 rows, 0.96 ms)
-// 0.19 is the stores', 0.77 remain where they go nowhere; workgroups that start apart from each other gain nothing.
+// 0.19 is the stores', 0.77 remain where they go nowhere; workgroups that start apart from each
+// other gain nothing, and half of a tile's stores between the next one's MFMAs lose (1.03).
 template <int OP, bool E8, bool OUT32, int BM, int BN, int WM, int WN, int D>
 __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_ragged_kernel(Fp8Args g) {
   constexpr int NW = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
