@@ -978,8 +978,8 @@ class _GroupedLinearFp8(torch.autograd.Function):
     """fp8_quant_ragged, fp8_quant_128x128, grouped_gemm_fp8 and grouped_gemm_fp8_wgrad on the parts of few buffers."""
 
     @staticmethod
-    def forward(ctx, x, w, offsets):
-        need_x, need_w = ctx.needs_input_grad[:2]
+    def forward(ctx, x, w, offsets, grad):
+        need_x, need_w = (grad and n for n in ctx.needs_input_grad[:2])
         f16 = _half(x, "x")
         R, K, ld = _matrix(x, "x")
         if w.dim() != 3 or w.shape[2] != K or not w.is_contiguous():
@@ -1022,7 +1022,7 @@ class _GroupedLinearFp8(torch.autograd.Function):
         if qt is not None:
             dw = dy.new_empty((E, N, K))
             _check(call.grouped_gemm_fp8_wgrad(dyt, dys, qt, ts, off, R, E, N, K, dw.data_ptr(), f16, stream))
-        return dx, dw, None
+        return dx, dw, None, None
 
 
 def grouped_linear_fp8(x, w, offsets):
@@ -1035,7 +1035,7 @@ def grouped_linear_fp8(x, w, offsets):
     """
     if x.dtype != w.dtype:
         raise ValueError("x and w must have the same type, got %s and %s" % (x.dtype, w.dtype))
-    return _GroupedLinearFp8.apply(x, w, offsets)
+    return _GroupedLinearFp8.apply(x, w, offsets, torch.is_grad_enabled())
 
 
 # ----------------------------------------------------------------- the layer

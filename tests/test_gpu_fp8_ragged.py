@@ -462,6 +462,21 @@ def test_linear_without_rows_with_strided_rows_and_twice(m):
         m.grouped_linear_fp8(b, odd, _dev([0, 10, 70]))
 
 
+def test_linear_without_gradients_keeps_nothing_for_them(m):
+    E, N, K, R = 4, 1024, 2048, 256
+    x, w = _randn((R, K), "bf16", 1).to(DEV).requires_grad_(), _randn((E, N, K), "bf16", 2).to(DEV).requires_grad_()
+    off, peak, out = _dev([0, 64, 128, 192, R]), [], []
+    for grad in (True, False):
+        torch.cuda.synchronize()
+        torch.cuda.reset_peak_memory_stats()
+        before = torch.cuda.memory_allocated()
+        with torch.set_grad_enabled(grad):
+            out.append(m.grouped_linear_fp8(x, w, off))
+        peak.append(torch.cuda.max_memory_allocated() - before)
+    assert out[0].requires_grad and not out[1].requires_grad and torch.equal(*out)
+    assert peak[1] <= peak[0] - E * N * K                                # the weights' codes transposed
+
+
 def test_linear_and_gradients_captured(m):
     """Forward and backward in one graph, on leaves made for each run."""
     E, N, K, R = 4, 144, 272, 300
@@ -568,6 +583,44 @@ def test_refusals(m):
                 lambda: m.grouped_gemm_fp8(xq[:, :24], xs, wq[:, :, :24].contiguous(), ws, d)):
         with pytest.raises(m.Moe355Error):
             bad()
+
+
+def _padded(t, off, most):
+    """[R, C] -> [E, most, C] in fp32, zeros behind each expert's rows."""
+    r = off[:-1, None] + torch.arange(most, device=DEV)
+    return torch.where((r < off[1:, None])[..., None], t.float()[r.clamp(max=max(len(t) - 1, 0))], 0.0)
+
+
+@pytest.mark.parametrize("E,R,N,K", [(513, 1500, 24, 32), (1500, 700, 136, 144), (65535, 70000, 8, 16), (600, 1200, 4104, 16), (5000, 33000, 520, 16),
+                                     (1500, 40000, 264, 272)])
+def test_many_experts_and_many_tiles_are_exact(m, E, R, N, K):
+    """More experts than a workgroup's table has entries, and more tiles than its stream holds: grids past the CUs.  Whole numbers up to 2
+    under scales of one, so every sum is exact: |y| <= 4 * 272 needs no rounding in fp32, and both sides round alike."""
+    g = torch.Generator().manual_seed(E)
+    c = torch.bincount(torch.randint(0, E, (R,), generator=g), minlength=E)
+    off = torch.cat([torch.zeros(1, dtype=torch.int64), c.cumsum(0)]).to(DEV)
+    x, w = torch.randint(-2, 3, (R, K), generator=g).to(DEV), torch.randint(-2, 3, (E, N, K), generator=g, dtype=torch.int8).to(DEV)
+    table = torch.tensor([0xc0, 0xb8, 0, 0x38, 0x40], dtype=torch.uint8, device=DEV)          # -2 .. 2
+    one = lambda *shape: torch.full(shape, 127, dtype=torch.uint8, device=DEV)
+    y = m.grouped_gemm_fp8(table[x + 2], one(R, -(-K // 128)), table[w.int() + 2], one(E, -(-N // 128), -(-K // 128)), off.int())
+    most = int(c.max())
+    ref = torch.bmm(_padded(x, off, most), w.float().transpose(1, 2).contiguous())
+    e = torch.repeat_interleave(torch.arange(E, device=DEV), c.to(DEV))
+    assert torch.equal(y, ref[e, torch.arange(R, device=DEV) - off[e]].to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("E,R,N,K", [(513, 1500, 24, 32), (9000, 12000, 136, 136), (65535, 70000, 8, 16)])
+def test_gradients_of_many_experts_are_exact(m, E, R, N, K):
+    g = torch.Generator().manual_seed(E)
+    c = torch.bincount(torch.randint(0, E, (R,), generator=g), minlength=E)
+    off = torch.cat([torch.zeros(1, dtype=torch.int64), c.cumsum(0)]).to(DEV)
+    x, dy = (torch.randint(-2, 3, (R, n), generator=g).to(DEV) for n in (K, N))
+    xt, dyt = (m.fp8_quant_ragged(t.to(torch.bfloat16), off.int(), rows=False)[2:] for t in (x, dy))
+    dw = m.grouped_gemm_fp8_wgrad(*dyt, *xt, off.int(), R, out_dtype=torch.bfloat16)
+    most = int(c.max())
+    assert most * 4 <= 256                                                # bf16 holds every sum
+    ref = torch.bmm(_padded(dy, off, most).transpose(1, 2).contiguous(), _padded(x, off, most))
+    assert torch.equal(dw.float(), ref)
 
 
 def test_row_offsets_past_two_to_the_32(m):
