@@ -671,6 +671,8 @@ def _elem(t, name, most=2):
 
 def _queue(*tensors):
     """The current GPU's stream, on which the kernels are queued: every tensor has to be on that GPU."""
+    if not tensors[0].is_cuda:
+        raise ValueError("tensors must be on a GPU, got one on %s" % tensors[0].device)
     dev = torch._C._cuda_getDevice()
     for t in tensors:
         if t is not None and t.get_device() != dev:

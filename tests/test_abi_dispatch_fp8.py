@@ -107,3 +107,19 @@ def test_product_codes(L):
     for bad in ({"d": _p(8)}, {"x": _p(8)}, {"dw": _p(8)}, {"off": _p(2)}):
         assert wgrad(**bad) == -3, bad
     assert wgrad(E=0, dw=None) == 0 and wgrad(N=0) == 0 and wgrad(K=0) == 0
+
+
+def test_tensors_off_the_gpu_are_refused(L):
+    """Before anything is launched, also where there is no GPU."""
+    import torch
+
+    import fp8_block_scaled_grouped_amd as m
+    ids, x, w = torch.zeros((4, 2), dtype=torch.int32), torch.zeros((4, 32), dtype=torch.bfloat16), torch.zeros((2, 16, 32), dtype=torch.bfloat16)
+    off, q = torch.tensor([0, 2, 4], dtype=torch.int32), torch.zeros((4, 32), dtype=torch.uint8)
+    for call in (lambda: m.moe_group(ids, 4), lambda: m.moe_dispatch(x, ids), lambda: m.moe_dispatch(x.float().requires_grad_(), ids),
+                 lambda: m.moe_combine(x, ids), lambda: m.moe_combine_grad(x, x, ids, torch.ones(4, 2)), lambda: m.fp8_quant_ragged(x, off),
+                 lambda: m.fp8_quant_128x128(w), lambda: m.grouped_linear_fp8(x, w, off),
+                 lambda: m.grouped_gemm_fp8(q, torch.ones(4, 1), torch.zeros((2, 16, 32), dtype=torch.uint8), torch.ones(2, 1, 1), off),
+                 lambda: m.grouped_gemm_fp8_wgrad(torch.zeros((2, 16, 128), dtype=torch.uint8), q, torch.zeros((2, 16, 128), dtype=torch.uint8), q, off, 4)):
+        with pytest.raises(ValueError):
+            call()
