@@ -8,7 +8,9 @@
 // C[m, n] = sum_s sa(m, s) sb(n, s) <A_s(m), B_s(n)> whose step s is a block of 128 codes: fwd's lie along the
 // rows of x and w, wgrad's in the transposed blocks [b][column][128] that fp8_quant_ragged writes, zeros past the segment's end.
 // A step is one 16x16x128 MFMA a 16 x 16 tile.  With power-of-two scales the MFMA applies them and adds to the fp32 sums; with
-// fp32 scales its result is folded in, acc += t * (sa * sb).
+// fp32 scales its result is folded in, acc += t * (sa * sb): the scales' product first, so one below 2^-126 is rounded to a multiple of
+// 2^-149 and its block off by less than 2^-125.  (Both scales' powers of two applied by the MFMA instead, and the rests folded, would
+// hold over all of fp32, and takes 5% longer: 1.70 ms against 1.60 below.)
 //
 // Ragged edges cost no branch in the loop: every LDS-DMA goes through a buffer descriptor that ends with
 // the operand's last valid byte, so rows past it arrive as zeros, and lanes whose chunk lies past the row's

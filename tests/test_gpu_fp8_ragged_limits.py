@@ -1,0 +1,61 @@
+"""FP8 operands and ragged expert products at the ends of their ranges, against the 64-bit oracle; tolerances as in
+test_gpu_fp8_ragged.py."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import fp8_ragged as o, ragged
+from tests import fp8_ragged_tilings as t
+from tests.test_gpu_fp8_ragged import DEV, _close, _dev, _offsets
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def m():
+    import fp8_block_scaled_grouped_amd as mod
+    mod.lib()
+    return mod
+
+
+# ------------------------------------------------------------------ fp32 scales
+# (binary exponents of x's scales, of w's, smallest code, codes): products of two scales below 2^-126 under sums of 2^23 and more, close to
+# 2^128 over sums of 2^-11 and less, and ordinary ones
+SCALES = [((-74, -72), (-74, -72), 0x78, 7), ((-140, -128), (-20, -4), 0x78, 7), ((-20, -4), (-140, -128), 0x78, 7),
+          ((64, 66), (56, 59), 0x01, 2), ((100, 104), (18, 21), 0x01, 2), ((-3, 3), (-3, 3), 0x30, 16)]
+ONE_OF_EACH = [t.PRODUCTS[i] for i in (1, 6, 9, 11)]
+
+
+@pytest.mark.parametrize("ex,ew,code,codes", SCALES)
+@pytest.mark.parametrize("counts,N,K", ONE_OF_EACH + [([3], 8, 16)])
+def test_products_of_scales_at_the_ends_of_fp32(m, counts, N, K, ex, ew, code, codes):
+    """Two scales are multiplied first, in fp32: below 2^-126 the product is off by up to 2^-150, so a block by that times its sum of
+    products of codes; each addition in that range by up to 2^-150 as well.  Codes of one sign, so sums are not small by chance."""
+    print("scales", counts[:4], N, K, ex, ew, flush=True)
+    E, R, KB, NB, g = len(counts), sum(counts), -(-K // 128), -(-N // 128), np.random.default_rng(N + K)
+    assert len({t.tile("fwd", sum(c), len(c), n, k) for c, n, k in ONE_OF_EACH}) == 4
+    off = _offsets(counts)
+    scale = lambda a, shape: np.ldexp(g.uniform(1, 2, shape), g.integers(a[0], a[1] + 1, shape)).astype(np.float32)
+    xs, ws = scale(ex, (R, KB)), scale(ew, (E, NB, KB))
+    xq, wq = (g.integers(code, code + codes, shape, dtype=np.uint8) for shape in ((R, K), (E, N, K)))
+    xs[0, 0], xq[R - 1] = 0, 0               # a block with a scale of zero, a row of zeros
+    y = m.grouped_gemm_fp8(*(torch.tensor(v, device=DEV) for v in (xq, xs, wq, ws)), _dev(off)).cpu()
+    ref, mag = ragged.forward(o.values(xq, xs, 1), o.values(wq, ws, 128), off)
+    sums = ragged.forward(o.fp8.decode(xq), o.fp8.decode(wq), off)[1]
+    each = o.each(xs, 1, R, K)
+    for e, (a, b) in enumerate(zip(off, off[1:])):
+        if a < b:
+            unit = o.unit_bound(xq[a:b], each[a:b], wq[e], o.each(ws[e], 128, N, K)) + (sums[a:b] + KB) * 2.0 ** -150
+            _close(y[a:b], ref[a:b], mag[a:b], K, "bf16", "y of expert %d" % e, unit)
+    assert (y[R - 1] == 0).all()
+
+
+def test_scales_of_zero_infinity_and_nan(m):
+    """Zero wins over any finite scale, infinities and NaN come through."""
+    K, N = 128, 16
+    code = torch.full((6, K), 0x7e, dtype=torch.uint8, device=DEV)
+    xs = torch.tensor([0.0, 1.0, float("inf"), float("nan"), -2.0, -float("inf")], device=DEV)[:, None]
+    for ws, finite in ((2.0 ** 126, False), (1.0, True), (2.0 ** -126, True)):
+        y = m.grouped_gemm_fp8(code, xs, code[:1].expand(1, N, K).contiguous(), torch.full((1, 1, 1), ws, device=DEV), _dev([0, 6])).float()
+        assert (y[0] == 0).all() and (y[2] == float("inf")).all() and y[3].isnan().all() and (y[5] == -float("inf")).all()
+        assert torch.isfinite(y[1]).all() == finite and torch.isfinite(y[4]).all() == finite and (y[4] < 0).all()
