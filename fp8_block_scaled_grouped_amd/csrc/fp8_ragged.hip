@@ -636,6 +636,7 @@ bool on4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 constexpr int64_t kMaxLd = 1 << 22;    // 256 rows' byte offsets stay below 2^31
 constexpr int kMaxDim = 1 << 22;
 constexpr int64_t kMaxSs = 1 << 21;    // and those of their scales
+constexpr int kMaxRows = 0x7fffffff - 255;  // row tiles of a segment are (rows + 255) / 256 in 32 bits
 
 }  // namespace
 }  // namespace moe355
@@ -648,7 +649,8 @@ extern "C" int grouped_gemm_fp8(const uint8_t* x8, const void* x_scale, int64_t 
   MOE355_CHECK((fp16 == 0 || fp16 == 1) && (e8m0 == 0 || e8m0 == 1) && R >= 0 && E >= 0 && N >= 0 && K >= 0 && ld_x >= K &&
                    ld_y >= N && sstride_m >= 0 && sstride_kb >= 0,
                MOE355_EINVAL);
-  MOE355_CHECK(N % 8 == 0 && K % 16 == 0 && N <= kMaxDim && E < 65536 && ld_x <= kMaxLd && sstride_m <= kMaxSs && ld_y <= kMaxSs, MOE355_EUNSUPPORTED);
+  MOE355_CHECK(N % 8 == 0 && K % 16 == 0 && N <= kMaxDim && E < 65536 && ld_x <= kMaxLd && sstride_m <= kMaxSs && ld_y <= kMaxSs && R <= kMaxRows,
+               MOE355_EUNSUPPORTED);
   if (R == 0 || E == 0 || N == 0) return MOE355_OK;
   MOE355_CHECK(offsets && y && (K == 0 || (x8 && w8 && x_scale && w_scale)), MOE355_EINVAL);
   MOE355_CHECK((K == 0 || (aligned16(x8) && ld_x % 16 == 0 && aligned16(w8))) && aligned16(y) && ld_y % 8 == 0 && on4(offsets) &&
@@ -661,7 +663,7 @@ extern "C" int grouped_gemm_fp8(const uint8_t* x8, const void* x_scale, int64_t 
 extern "C" int grouped_gemm_fp8_wgrad(const uint8_t* dyt, const uint8_t* dyt_scale, const uint8_t* xt, const uint8_t* xt_scale,
                                       const int32_t* offsets, int R, int E, int N, int K, void* dw, int out, hipStream_t stream) {
   MOE355_CHECK(R >= 0 && E >= 0 && N >= 0 && K >= 0 && out >= MOE355_BF16 && out <= MOE355_F32, MOE355_EINVAL);
-  MOE355_CHECK(N % 8 == 0 && K % 8 == 0 && N <= kMaxDim && K <= kMaxDim && E < 65536, MOE355_EUNSUPPORTED);
+  MOE355_CHECK(N % 8 == 0 && K % 8 == 0 && N <= kMaxDim && K <= kMaxDim && E < 65536 && R <= kMaxRows, MOE355_EUNSUPPORTED);
   if (E == 0 || N == 0 || K == 0) return MOE355_OK;  // without rows every gradient is zero: still written
   MOE355_CHECK(offsets && dw && (R == 0 || (dyt && dyt_scale && xt && xt_scale)), MOE355_EINVAL);
   MOE355_CHECK((R == 0 || (aligned16(dyt) && aligned16(xt))) && aligned16(dw) && on4(offsets), MOE355_EMISALIGNED);

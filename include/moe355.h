@@ -520,7 +520,7 @@ int fp8_quant_128x128(const uint16_t* w, int fp16, int E, int N, int K, uint8_t*
  * multiplied first, so where their product is below 2^-126 a block is off by up to 2^-150 times its sum of |x8 * w8| (less than 2^-125),
  * and where it is 2^128 or more the block is infinite, or NaN if its sum is zero; with E8M0 scales what lies below 2^-126 may be lost.
  * grouped_gemm_fp8: N % 8 == 0, K % 16 == 0, ld_x and N up to 4194304, ld_y and sstride_m up to 2097152; wgrad: N % 8 == 0,
- * K % 8 == 0, both up to 4194304; E < 65536; else MOE355_EUNSUPPORTED.  Pointers 16-byte aligned (fp32 scales and offsets 4,
+ * K % 8 == 0, both up to 4194304; E < 65536 and R up to 2^31 - 256; else MOE355_EUNSUPPORTED.  Pointers 16-byte aligned (fp32 scales and offsets 4,
  * E8M0 scales any: they are read with the rest of the aligned 4 bytes that hold them), ld_x a multiple of 16 and ld_y of 8, else
  * MOE355_EMISALIGNED.
  */
