@@ -438,6 +438,7 @@ extern "C" int moe_combine_grad(const void* dout, int64_t ld_dout, const void* r
   MOE355_CHECK(dtype >= MOE355_BF16 && dtype <= MOE355_F32 && T >= 0 && H >= 0 && topk >= 1 && R >= 0 && ld_dout >= H &&
                    (!dweights || ld_rows >= H) && (!drows || ld_drows >= H) && ld_weights >= topk,
                MOE355_EINVAL);
+  MOE355_CHECK(H <= 0x7fffffff - 255, MOE355_EUNSUPPORTED);  // a lane's next vector is counted in 32 bits
   if (T == 0 || (!drows && !dweights)) return MOE355_OK;
   MOE355_CHECK((H == 0 || dout) && (!dweights || R == 0 || H == 0 || rows) && row_of_pair && weights, MOE355_EINVAL);
   const int sz = size_of(dtype);

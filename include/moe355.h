@@ -465,7 +465,8 @@ int moe_group(const int32_t* topk_ids, int64_t ld_topk, int T, int topk, int E, 
  *                     dweights[t, j] = sum_h dout[t, h] * rows[row_of_pair[t, j], h]   (fp32; 0 without a row)
  * x, out, dout [T, H], rows, drows [R, H]: MOE355_BF16, _F16 or _F32 (moe_dispatch also _U8), row strides ld_*.
  * weights fp32 [T, topk], row stride ld_weights; dweights fp32 [T, topk].  drows or dweights may be NULL.
- * No two pairs share a row.  Any H; rows that start on 16 bytes and hold a multiple of 16 are faster.
+ * No two pairs share a row.  Any H (moe_combine_grad: up to 2^31 - 256, else MOE355_EUNSUPPORTED); rows
+ * that start on 16 bytes and hold a multiple of 16 are faster.
  * Every sum has a fixed order.
  */
 int moe_dispatch(const void* x, int dtype, int64_t ld_x, int T, int H, int topk, const int32_t* row_of_pair,
