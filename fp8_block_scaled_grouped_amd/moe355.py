@@ -669,6 +669,14 @@ def _elem(t, name, most=2):
     return n
 
 
+_MOST = 2 ** 31 - 1
+
+
+def _cut(*sizes):
+    """Sizes that the library's 32-bit arguments would cut."""
+    raise ValueError("sizes must be below 2^31, got %s" % (sizes,))
+
+
 def _queue(*tensors):
     """The current GPU's stream, on which the kernels are queued: every tensor has to be on that GPU."""
     if not tensors[0].is_cuda:
@@ -684,6 +692,8 @@ def _pairs(row_of_pair):
     shape = row_of_pair.shape
     if len(shape) != 2 or shape[1] < 1 or row_of_pair.dtype != torch.int32 or not row_of_pair.is_contiguous():
         raise ValueError("row_of_pair must be a contiguous int32 tensor [T, topk], got %s %s" % (row_of_pair.dtype, tuple(shape)))
+    if shape[0] | shape[1] > _MOST:
+        _cut(*shape)
     return shape
 
 
@@ -692,6 +702,8 @@ def _matrix(t, name):
     shape = t.shape
     if len(shape) != 2:
         raise ValueError("%s must be 2-D, got %s" % (name, tuple(shape)))
+    if shape[0] | shape[1] > _MOST:
+        _cut(*shape)
     return shape[0], shape[1], shape[1] if t.is_contiguous() else _ld(t, name)
 
 
@@ -705,6 +717,8 @@ def _grad_wanted(*tensors):
 @functools.lru_cache(maxsize=256)
 def moe_group_workspace(T, topk, E):
     """Bytes of workspace that moe_group needs (host-only)."""
+    if T | topk | E > _MOST:
+        _cut(T, topk, E)
     b = ctypes.c_size_t()
     _check(lib().moe_group_workspace(T, topk, E, ctypes.byref(b)))
     return b.value
@@ -719,6 +733,8 @@ def moe_group(topk_ids, E, out=None, workspace=None):
     if topk_ids.dtype != torch.int32:
         raise ValueError("topk_ids must be int32, got %s" % topk_ids.dtype)
     T, k, ld = _matrix(topk_ids, "topk_ids")
+    if E > _MOST:
+        _cut(E)
     n = T * k
     stream = _queue(topk_ids, *out or (), workspace)
     if out is None:
@@ -761,11 +777,13 @@ def moe_dispatch(x, row_of_pair, rows=None):
     if n != T:
         raise ValueError("x must have the %d tokens of row_of_pair, got %d" % (T, n))
     if rows is None:
+        if T * k > _MOST:
+            _cut(T * k)
         stream = _queue(x, row_of_pair)
         R, ld_rows, rows = T * k, H, x.new_empty((T * k, H))
     else:
-        stream = _queue(x, row_of_pair, rows)
         R, w, ld_rows = _matrix(rows, "rows")
+        stream = _queue(x, row_of_pair, rows)
         if w != H or rows.dtype != x.dtype:
             raise ValueError("rows must be [R, %d] in the type of x" % H)
     _check(lib().moe_dispatch(x.data_ptr(), dt, ld, T, H, k, row_of_pair.data_ptr(), R, rows.data_ptr(), ld_rows, stream))
@@ -851,6 +869,8 @@ def moe_combine_grad(dout, rows, row_of_pair, weights, drows=None, dweights=None
 # ----------------------------------------------------------------- FP8 products over ragged groups
 def fp8_ragged_blocks(R, E):
     """Number of 128-row blocks that fp8_quant_ragged's transposed output has room for (host-only)."""
+    if R | E > _MOST:
+        _cut(R, E)
     n = ctypes.c_int64()
     _check(lib().fp8_ragged_blocks(R, E, ctypes.byref(n)))
     return n.value
@@ -867,6 +887,8 @@ def fp8_quant_ragged(x, offsets=None, rows=True, columns=True):
     f16 = _half(x, "x")
     ld = _ld(x, "x")
     R, K = x.shape
+    if R | K > _MOST:
+        _cut(R, K)
     columns = columns and offsets is not None
     E = 0
     if offsets is not None:
@@ -899,6 +921,8 @@ def fp8_quant_128x128(w, scale_format="e8m0", transposed=False):
     if w.dim() != 3 or not w.is_contiguous():
         raise ValueError("w must be a contiguous [E, N, K] tensor")
     E, N, K = w.shape
+    if E | N | K > _MOST:
+        _cut(E, N, K)
     sdt = torch.uint8 if scale_format == "e8m0" else torch.float32
     q, scale = w.new_empty((E, N, K), dtype=torch.uint8), w.new_empty((E, _nblk(N), _nblk(K)), dtype=sdt)
     qt = tscale = None
@@ -923,6 +947,8 @@ def grouped_gemm_fp8(x8, x_scale, w8, w_scale, offsets, y=None, out_dtype=torch.
     ld = _ld(x8, "x8")
     R, K = x8.shape
     E, N, wK = w8.shape
+    if R | E | N | K > _MOST:
+        _cut(R, E, N, K)
     NB, KB = _nblk(N), _nblk(K)
     if wK != K or not w8.is_contiguous():
         raise ValueError("w8 must be a contiguous [E, N, %d], got %s" % (K, tuple(w8.shape)))
@@ -950,6 +976,8 @@ def grouped_gemm_fp8_wgrad(dyt, dyt_scale, xt, xt_scale, offsets, R, dw=None, ou
     E = offsets.shape[0] - 1
     _need(offsets, (E + 1,), torch.int32, "offsets")
     blocks, N, K = fp8_ragged_blocks(R, E), dyt.shape[1], xt.shape[1]
+    if E | N | K > _MOST:
+        _cut(E, N, K)
     for t, shape, name in ((dyt, (blocks, N, 128), "dyt"), (dyt_scale, (blocks, N), "dyt_scale"), (xt, (blocks, K, 128), "xt"),
                            (xt_scale, (blocks, K), "xt_scale")):
         _need(t, shape, torch.uint8, name)
@@ -987,6 +1015,8 @@ class _GroupedLinearFp8(torch.autograd.Function):
         if w.dim() != 3 or w.shape[2] != K or not w.is_contiguous():
             raise ValueError("w must be a contiguous [E, N, %d] tensor, got %s" % (K, tuple(w.shape)))
         E, N, _ = w.shape
+        if E | N > _MOST:
+            _cut(E, N)
         if offsets.dtype != torch.int32 or offsets.shape != (E + 1,) or not offsets.is_contiguous():
             raise ValueError("offsets must be a contiguous int32 tensor of %d, got %s %s" % (E + 1, offsets.dtype, tuple(offsets.shape)))
         stream, off, call = _queue(x, w, offsets), offsets.data_ptr(), lib()

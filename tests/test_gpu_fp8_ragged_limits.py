@@ -59,3 +59,16 @@ def test_scales_of_zero_infinity_and_nan(m):
         y = m.grouped_gemm_fp8(code, xs, code[:1].expand(1, N, K).contiguous(), torch.full((1, 1, 1), ws, device=DEV), _dev([0, 6])).float()
         assert (y[0] == 0).all() and (y[2] == float("inf")).all() and y[3].isnan().all() and (y[5] == -float("inf")).all()
         assert torch.isfinite(y[1]).all() == finite and torch.isfinite(y[4]).all() == finite and (y[4] < 0).all()
+
+
+def test_sizes_that_32_bits_would_cut_are_refused(m):
+    """The library's sizes are C ints: 2^32 + n must not pass for n."""
+    row, off = torch.zeros((1, 16), dtype=torch.bfloat16, device=DEV), _dev([0, 16])
+    z = lambda *shape: torch.zeros(shape, dtype=torch.uint8, device=DEV)
+    many = row.expand(2 ** 32 + 16, 16)
+    w = torch.empty((1, 1, 2 ** 32 + 128), dtype=torch.bfloat16, device=DEV)
+    for call in (lambda: m.fp8_quant_ragged(many), lambda: m.fp8_quant_ragged(many, off), lambda: m.fp8_quant_128x128(w),
+                 lambda: m.grouped_linear_fp8(many, torch.zeros((1, 16, 16), dtype=torch.bfloat16, device=DEV), off),
+                 lambda: m.grouped_gemm_fp8_wgrad(z(1, 16, 128), z(1, 16), z(1, 16, 128), z(1, 16), off, 2 ** 32 + 16)):
+        with pytest.raises(ValueError, match=r"below 2\^31"):
+            call()
