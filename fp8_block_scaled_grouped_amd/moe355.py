@@ -794,20 +794,21 @@ class _Combine(torch.autograd.Function):
     @staticmethod
     def forward(ctx, rows, row_of_pair, weights):
         ctx.rows = rows.shape[0]
-        ctx.save_for_backward(row_of_pair, *(() if weights is None else (weights, rows)))
+        # the rows themselves are only in the gradient of the weights
+        ctx.save_for_backward(row_of_pair, weights, rows if ctx.needs_input_grad[2] else None)
         return moe_combine(rows, row_of_pair, weights)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dout):
-        row_of_pair, *rest = ctx.saved_tensors
+        row_of_pair, weights, rows = ctx.saved_tensors
         dout = dout.contiguous()
         # rows that no pair has get a gradient of zeros
         drows = dout.new_zeros((ctx.rows, dout.shape[1])) if ctx.needs_input_grad[0] else None
-        if not rest:
+        if weights is None:
             return moe_dispatch(dout, row_of_pair, drows), None, None
-        weights, rows = rest
-        drows, dw = moe_combine_grad(dout, rows, row_of_pair, weights, drows, want=ctx.needs_input_grad[0::2])
+        # (without a gradient of the weights the rows are not read)
+        drows, dw = moe_combine_grad(dout, drows if rows is None else rows, row_of_pair, weights, drows, want=ctx.needs_input_grad[0::2])
         return drows, None, dw
 
 
