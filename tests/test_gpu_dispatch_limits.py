@@ -1,5 +1,4 @@
 """Dispatch and combine: what autograd keeps, and the largest sizes; oracles and tolerances as in test_gpu_dispatch.py."""
-import numpy as np
 import pytest
 import torch
 
@@ -44,3 +43,38 @@ def test_rows_are_kept_for_the_gradient_of_the_weights_alone(m, T, k, H):
         rows.zero_()
     with pytest.raises(RuntimeError):
         torch.autograd.grad(out, (leaf, w), dout)
+
+
+# ------------------------------------------------------------------ many pairs
+def _sorted(ids, E):
+    """The oracle's order by torch's stable sort (its own loop is long)."""
+    flat = ids.reshape(-1).long()
+    key, order = torch.sort(torch.where((flat >= 0) & (flat < E), flat, E), stable=True)
+    off, n = torch.searchsorted(key, torch.arange(E + 1)), int((key < E).sum())
+    rop = torch.full((flat.numel(),), -1)
+    rop[order[:n]] = torch.arange(n)
+    return off, rop.view(ids.shape), torch.where(key < E, order, -1)
+
+
+# chunks are of 4096 pairs up to 256 of them; past 1048576 pairs of 8192 and more, whose waves hold 256 ids in registers and read the others
+# twice: parts of 512, 768 (the last ones cut short) and 512 with all experts that there may be
+@pytest.mark.parametrize("T,k,E", [(131072, 8, 256), (131073, 8, 256), (300001, 8, 256), (150011, 7, 1024), (1100000, 1, 3)])
+def test_group_of_more_than_a_million_pairs(m, T, k, E):
+    print("group", T, k, E, flush=True)
+    ids = _ids(T, k, E, T)
+    ref = _sorted(ids, E)
+    wide = torch.full((T, k + 3), 77, dtype=torch.int32)      # rows with a stride
+    wide[:, :k] = ids
+    for x in (ids.to(DEV), wide.to(DEV)[:, :k]):
+        for got, want in zip(m.moe_group(x, E), ref):
+            assert torch.equal(got.cpu().long(), want)
+
+
+@pytest.mark.parametrize("T,k,E", [(140000, 8, 16)])
+def test_group_of_more_than_a_million_pairs_on_one_expert_and_on_none(m, T, k, E):
+    one = torch.full((T, k), E - 1, dtype=torch.int32, device=DEV)
+    o, r, p = m.moe_group(one, E)
+    assert o.tolist() == [0] * E + [T * k] and torch.equal(r.flatten(), torch.arange(T * k, device=DEV, dtype=torch.int32))
+    assert torch.equal(p, r.flatten())
+    o, r, p = m.moe_group(torch.full_like(one, E), E)
+    assert o.tolist() == [0] * (E + 1) and (r == -1).all() and (p == -1).all()
