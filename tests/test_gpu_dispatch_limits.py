@@ -78,3 +78,23 @@ def test_group_of_more_than_a_million_pairs_on_one_expert_and_on_none(m, T, k, E
     assert torch.equal(p, r.flatten())
     o, r, p = m.moe_group(torch.full_like(one, E), E)
     assert o.tolist() == [0] * (E + 1) and (r == -1).all() and (p == -1).all()
+
+
+def test_gradients_of_rows_past_two_to_the_31_bytes(m):
+    """The last rows of two buffers of 4.3 GB: gradients of rows and weights.  Multiples of 1/4 up to 2 (rows) and 1 (dout), so a product is a
+    multiple of 1/16 and sums of H = 2^15 of them, below 2^16, are exact in fp32 in any order."""
+    T, k, H = 4, 2, 1 << 15
+    R = (1 << 32) // (2 * H) + 64
+    rows, drows = (torch.zeros((R, H), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    rop = torch.tensor([[R - 1, 0], [R - 2, 1], [R // 2, R // 2 + 1], [R - 64, 7]], dtype=torch.int32, device=DEV)
+    g = torch.Generator().manual_seed(1)
+    y = torch.randint(-8, 9, (T, k, H), generator=g).to(DEV) / 4
+    dout = torch.randint(-4, 5, (T, H), generator=g).to(DEV) / 4
+    rows[rop.long()] = y.to(torch.bfloat16)
+    w = torch.tensor([[0.5, 1.0], [2.0, 0.25], [1.0, 4.0], [0.125, 8.0]], device=DEV)
+    d, dw = m.moe_combine_grad(dout.to(torch.bfloat16), rows, rop, w, drows)
+    assert d is drows and torch.equal(dw, (y * dout[:, None]).sum(-1))
+    assert torch.equal(drows[rop.long()], (w[..., None] * dout[:, None]).to(torch.bfloat16))
+    rest = torch.ones(R, dtype=torch.bool, device=DEV)
+    rest[rop.long().flatten()] = False
+    assert not drows.any(1)[rest].any()

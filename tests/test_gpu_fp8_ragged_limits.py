@@ -72,3 +72,77 @@ def test_sizes_that_32_bits_would_cut_are_refused(m):
                  lambda: m.grouped_gemm_fp8_wgrad(z(1, 16, 128), z(1, 16), z(1, 16, 128), z(1, 16), off, 2 ** 32 + 16)):
         with pytest.raises(ValueError, match=r"below 2\^31"):
             call()
+
+
+# ------------------------------------------------------------------ offsets past 4 GiB
+ONE = 0x38                                                                # the code of 1.0
+
+
+def _bytes(shape, value):
+    return torch.full(shape, value, dtype=torch.uint8, device=DEV)
+
+
+def test_outputs_past_two_to_the_32_bytes(m):
+    E, N, K = 3, 1 << 15, 16
+    R = (1 << 32) // (2 * N) + 300
+    off = [0, R - 260, R - 130, R]
+    x8 = _bytes((R, K), 0)
+    x8[R - 260:] = ONE
+    ws = _bytes((E, N // 128, 1), 127)
+    ws[2] = 128
+    y = m.grouped_gemm_fp8(x8, _bytes((1, 1), 127).expand(R, 1), _bytes((E, N, K), ONE), ws, _dev(off))
+    assert not y[:R - 260].any() and (y[R - 260:R - 130] == K).all() and (y[R - 130:] == 2 * K).all()
+
+
+def test_weights_past_two_to_the_32_bytes(m):
+    """Weights of 4.3 GB: quantised, both ways, and the last two experts multiplied, by two tiles."""
+    E, N, K = 66, 1 << 12, 1 << 14
+    w = torch.zeros((E, N, K), dtype=torch.bfloat16, device=DEV)
+    w[E - 1], w[E - 2, -1] = 1.0, 2.0
+    q, s, qt, ts = m.fp8_quant_128x128(w, transposed=True)
+    del w
+    # the smallest power of two that keeps 1 (2) in +-448 is 2^-8 (2^-7), 256 of which is code 0x78
+    assert (q[E - 1] == 0x78).all() and (q[E - 2, -1] == 0x78).all() and not q[:E - 2].any() and not q[E - 2, :-1].any()
+    assert (qt[E - 1] == 0x78).all() and (qt[E - 2, :, -1] == 0x78).all() and not qt[:E - 2].any() and not qt[E - 2, :, :-1].any()
+    assert (s[E - 1] == 119).all() and (ts[E - 1] == 119).all() and (s[:E - 2] == 127).all() and (ts[:E - 2] == 127).all()
+    assert (s[E - 2, -1] == 120).all() and (s[E - 2, :-1] == 127).all() and (ts[E - 2, :, -1] == 120).all() and (ts[E - 2, :, :-1] == 127).all()
+    del qt
+    for n in (3, 3000):
+        off = [0] * (E - 2) + [0, n, 2 * n]
+        y = m.grouped_gemm_fp8(_bytes((2 * n, K), ONE), _bytes((1, 1), 127).expand(2 * n, K // 128), q, s, _dev(off))
+        assert not y[:n, :-1].any() and (y[:n, -1] == 2 * K).all() and (y[n:] == K).all()
+
+
+@pytest.mark.parametrize("N,K", [(16, 1 << 15), (1 << 15, 16)])
+def test_codes_and_blocks_past_two_to_the_32_bytes(m, N, K):
+    """Rows' codes and transposed blocks of 4.3 GB, written and multiplied: those of x, and those of dy."""
+    E, wide = 3, 1 << 15
+    R = (1 << 32) // wide + 300
+    off = [0, R - 260, R - 130, R]
+    t = torch.zeros((R, wide), dtype=torch.bfloat16, device=DEV)
+    t[R - 260:] = 1
+    q, s, qt, ts = m.fp8_quant_ragged(t, _dev(off))
+    del t
+    assert (q[R - 260:] == 0x78).all() and not q[:R - 260].any() and (s[R - 260:] == 119).all() and (s[:R - 260] == 127).all()
+    b = [off[e] // 128 + e for e in (1, 2)]                                # blocks of the last experts: 128 rows and 2
+    for first in b:
+        assert (qt[first] == 0x78).all() and (qt[first + 1, :, :2] == 0x78).all() and not qt[first + 1, :, 2:].any()
+        assert (ts[first:first + 2] == 119).all()
+    assert not qt[:off[1] // 128].any() and (ts[:off[1] // 128] == 127).all()
+    del q, s
+    _, _, ot, ots = m.fp8_quant_ragged(torch.ones((R, 16), dtype=torch.bfloat16, device=DEV), _dev(off), rows=False)
+    args = (qt, ts, ot, ots) if N > K else (ot, ots, qt, ts)
+    dw = m.grouped_gemm_fp8_wgrad(*args, _dev(off), R)
+    assert not dw[0].any() and (dw[1:] == 130).all()
+
+
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+def test_gradients_of_weights_past_two_to_the_32_bytes(m, out):
+    E, N, K, R = 3, 1 << 15, 1 << 15, 130
+    off = _dev([0, 1, 1, R])
+    dy, x = (torch.ones((R, n), dtype=torch.bfloat16, device=DEV) for n in (N, K))
+    dy[R - 1, -1] = 3
+    (dyt, dys), (xt, xs) = (m.fp8_quant_ragged(v, off, rows=False)[2:] for v in (dy, x))
+    dw = m.grouped_gemm_fp8_wgrad(dyt, dys, xt, xs, off, R, out_dtype=out)
+    assert (dw[0] == 1).all() and not dw[1].any() and (dw[2, :-1] == R - 1).all()
+    assert (dw[2, -1] == torch.tensor(R + 1.0).to(out)).all()
