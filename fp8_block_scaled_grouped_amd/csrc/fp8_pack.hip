@@ -57,8 +57,8 @@ struct Tile {
 };
 
 // Codes of the four values in two words with the scale of E8M0 byte c.  The conversion divides by the power of two and rounds
-// once: for every 16-bit value and byte that keep it in +-448 the same code as the product with 2^(127 - c) rounded by
-// f32x4_to_e4m3, NaN for byte 255 (all 65536 x 256 of either type compared), and one instruction in place of nine a pair.
+// once (held by a test for every value under every byte that its block can have; byte 0, here a scale of +0, counts as 2^-127), NaN for
+// byte 255, and takes one instruction in place of nine a pair.
 template <bool F16>
 __device__ __forceinline__ uint32_t codes4(uint32_t lo, uint32_t hi, uint32_t c) {
   const float s = __uint_as_float(c << 23);

@@ -6,7 +6,7 @@ import torch
 
 from oracle import fp8_ragged as o, ragged
 from tests import fp8_ragged_tilings as t
-from tests.test_gpu_fp8_ragged import DEV, _close, _dev, _offsets
+from tests.test_gpu_fp8_ragged import DEV, DT, _close, _dev, _offsets
 
 pytestmark = pytest.mark.gpu
 
@@ -146,3 +146,57 @@ def test_gradients_of_weights_past_two_to_the_32_bytes(m, out):
     dw = m.grouped_gemm_fp8_wgrad(dyt, dys, xt, xs, off, R, out_dtype=out)
     assert (dw[0] == 1).all() and not dw[1].any() and (dw[2, :-1] == R - 1).all()
     assert (dw[2, -1] == torch.tensor(R + 1.0).to(out)).all()
+
+
+# ------------------------------------------------------------------ every value under every scale
+def _bits(first, end, dt):
+    return torch.arange(first, end, dtype=torch.int32).to(torch.int16).view(dt)
+
+
+def _blocks(dt, n):
+    """Blocks of n values whose first is the largest magnitude with an E8M0 byte, the others all values up to it with both signs, and the
+    byte of each block: every pair of a value and a byte that quantisation can bring together."""
+    mags = _bits(0, 0x7f80 if dt == torch.bfloat16 else 0x7c00, dt)
+    byte = torch.from_numpy(o.e8m0_byte(mags.double().numpy())).long()
+    blocks, bytes_ = [], []
+    for c in byte[1:].unique().tolist():                                   # (zero has a byte of its own, which others have too)
+        last = int((byte[1:] == c).nonzero().max()) + 1                    # magnitudes ascend with their bits
+        some = torch.cat([mags[:last + 1], -mags[:last + 1]])
+        some = torch.nn.functional.pad(some, (0, -some.numel() % (n - 1))).view(-1, n - 1)
+        blocks.append(torch.cat([mags[last].expand(some.shape[0], 1), some], 1))
+        bytes_ += [c] * some.shape[0]
+    return torch.cat(blocks), np.array(bytes_, np.uint8), byte
+
+
+@pytest.mark.parametrize("dtype,first,last", [("bf16", 0, 247), ("fp16", 95, 135)])
+def test_every_value_under_every_scale_that_its_block_can_have(m, dtype, first, last):
+    """All bytes from the smallest subnormal's (bf16: 0, where the scale is kept at 2^-127) to the largest finite value's."""
+    dt = DT[dtype]
+    x, c, byte = _blocks(dt, 128)
+    assert set(c.tolist()) == set(range(first, last + 1))
+    ref = o.fp8.encode(x.double().numpy() / o.e8m0_value(c)[:, None])
+    q, s, _, _ = m.fp8_quant_ragged(x.to(DEV), columns=False)
+    assert (s[:, 0].cpu().numpy() == c).all() and (q.cpu().numpy() == ref).all()
+    xt = x.t()[:, :x.shape[0] // 8 * 8].contiguous()                       # the same blocks as columns of 128 rows
+    _, _, qt, ts = m.fp8_quant_ragged(xt.to(DEV), _dev([0, 128]), rows=False)
+    n = xt.shape[1]
+    assert (ts[0].cpu().numpy() == c[:n]).all() and (qt[0].cpu().numpy() == ref[:n]).all()
+    w, c, _ = _blocks(dt, 128 * 128)
+    q, s, qt, ts = m.fp8_quant_128x128(w.view(-1, 128, 128).to(DEV), transposed=True)
+    ref = o.fp8.encode(w.double().numpy() / o.e8m0_value(c)[:, None]).reshape(-1, 128, 128)
+    assert (s.flatten().cpu().numpy() == c).all() and (q.cpu().numpy() == ref).all()
+    assert torch.equal(qt, q.transpose(1, 2)) and torch.equal(ts, s)
+
+
+@pytest.mark.parametrize("dtype,end", [("bf16", 0x7f80), ("fp16", 0x7c00)])
+def test_every_magnitude_as_the_largest_of_a_block(m, dtype, end):
+    """The bytes of blocks whose largest magnitude is each finite value, and 255 for infinity and every NaN, alone in a block of zeros."""
+    v = _bits(0, 0x8000, DT[dtype])
+    want = np.where(np.arange(0x8000) < end, o.e8m0_byte(v.double().nan_to_num(0).numpy()), 255)
+    for sign in (1, -1):
+        x = torch.zeros((0x8000, 128), dtype=DT[dtype])
+        x[:, 77] = v if sign > 0 else (v.view(torch.int16) | -0x8000).view(DT[dtype])
+        _, s, _, ts = m.fp8_quant_ragged(x.t().contiguous().to(DEV), _dev([0, 128]))
+        assert (ts[0].cpu().numpy() == want).all()
+        _, s, _, _ = m.fp8_quant_ragged(x.to(DEV), columns=False)
+        assert (s[:, 0].cpu().numpy() == want).all()
