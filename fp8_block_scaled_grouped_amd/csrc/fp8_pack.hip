@@ -6,8 +6,10 @@
 // the input is read once for both orientations.  The maxima are those of the magnitudes'
 // 16 bits (they order as the values do, infinities and NaN above all).  The codes of
 // 8 rows of a column are 8 bytes of the transposed tile, which goes through LDS to be stored in whole lines.
-// Bound by memory: 2 bytes in, 1 or 2 out for each value.  Both orientations of 32768 x 7168 190 us (4.9 TB/s), of weights 32 x 4096 x 7168
-// 735 us (5.1 TB/s).  A few thousand rows wait for their own latencies: 5003 x 1168 over 48 experts 11.5 us (2 TB/s; rows or columns alone 7).
+// Bound by memory: 2 bytes in, 1 or 2 out for each value.  Both orientations of 32768 x 7168 161 to 196 us (4.8 to 5.8 TB/s), of weights
+// 32 x 4096 x 7168 705 to 735 us (5.1 to 5.3 TB/s; as stored alone 515 to 540), with fp32 scales the same.  A few thousand rows wait for their
+// own latencies: 5003 x 1168 over 48 experts 11 us run over and over (2.1 TB/s; rows or columns alone 7), 14 behind the launches of a
+// training step, 17 with nothing in the caches.
 //
 // Scales.  E8M0: byte c stands for 2^(c - 127), the smallest power of two that keeps the block in +-448
 // (448 = 1.75 * 2^8), so nothing saturates and codes are the nearest e4m3 of x * 2^(127 - c), rounded

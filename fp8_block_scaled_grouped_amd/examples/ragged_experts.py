@@ -74,6 +74,7 @@ class RaggedExperts(torch.nn.Module):
         if self.fp8:
             offsets, row_of_pair, _ = m.moe_group(ids, self.E)
             h = silu_mul(self.experts(m.moe_dispatch(x, row_of_pair), "w1", offsets))
+            # summed in fp32 and rounded to the rows' bf16, once, before the shared expert is added (the sum below stays fp32)
             out = m.moe_combine(self.experts(h, "w2", offsets), row_of_pair, weights).float()
             return out + self.shared(silu_mul(self.shared(x, "s1")), "s2").float()
         order, offsets = group_by_expert(ids, self.E)

@@ -53,7 +53,7 @@ def _randn(shape, dtype, seed, std=1.0):
 
 
 # ------------------------------------------------------------------ grouping
-# one workgroup up to 4096 pairs, chunks of 1024 beyond; experts off and on powers of two, more than the threads of a workgroup
+# one workgroup up to 4096 pairs, chunks of 4096 beyond; experts off and on powers of two, up to as many as a workgroup has threads
 @pytest.mark.parametrize("T,k,E", [(0, 2, 5), (1, 1, 1), (1, 8, 256), (3, 5, 7), (64, 8, 256), (100, 3, 1024), (512, 8, 64), (4096, 1, 2),
                                    (4097, 1, 3), (700, 6, 257), (3001, 8, 1024), (9000, 7, 33), (40000, 8, 256)])
 def test_group(m, T, k, E):
