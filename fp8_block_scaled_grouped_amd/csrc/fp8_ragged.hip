@@ -504,7 +504,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_ragged_kernel(Fp8Args g) 
         } else {
           // ahead of each MFMA the fold of the tile three before it: the unit is never waited for (65536 rows at random over 32 experts
           // of 4096 x 7168, rounded normal values under scales of one, 1.65 ms; behind the MFMA and two before 1.69, one before 1.76.  On
-          // quantised values, which cost more power, 1.75 either way)
+          // quantised values, which cost more power, 1.74 to 1.81 either way)
           const int q = j * TM + i;
           if (q >= 3) fold(q - 3);
           acc2[q % 4] = mfma16x16x128_fp8(rb[j % kHold], ra[PAR][i], zero);

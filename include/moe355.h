@@ -465,8 +465,10 @@ int moe_group(const int32_t* topk_ids, int64_t ld_topk, int T, int topk, int E, 
  *                     dweights[t, j] = sum_h dout[t, h] * rows[row_of_pair[t, j], h]   (fp32; 0 without a row)
  * x, out, dout [T, H], rows, drows [R, H]: MOE355_BF16, _F16 or _F32 (moe_dispatch also _U8), row strides ld_*.
  * weights fp32 [T, topk], row stride ld_weights; dweights fp32 [T, topk].  drows or dweights may be NULL.
- * No two pairs share a row.  Any H (moe_combine_grad: up to 2^31 - 256, else MOE355_EUNSUPPORTED); rows
- * that start on 16 bytes and hold a multiple of 16 are faster.
+ * No two pairs share a row.  Any H; rows that start on 16 bytes and hold a multiple of 16 are faster.  Larger calls
+ * than these are MOE355_EUNSUPPORTED: moe_dispatch and moe_combine T * ceil(v / 64) up to 67108860, with v the vectors of a row (16 bytes,
+ * or where rows do not allow that an element, of moe_dispatch 4 or 2 bytes if they do); moe_combine_grad T * topk up to 67108860 and H
+ * up to 2^31 - 256.
  * Every sum has a fixed order.
  */
 int moe_dispatch(const void* x, int dtype, int64_t ld_x, int T, int H, int topk, const int32_t* row_of_pair,
@@ -491,12 +493,14 @@ int moe_combine_grad(const void* dout, int64_t ld_dout, const void* rows, int64_
  *               blocks start at offsets[e]/128 + e and blocks = fp8_ragged_blocks(R, E) (some stay unused
  *               and are not written); rows past the segment's end are zeros.
  * Either pair may be NULL.  With offsets NULL the rows are one segment (q and scale only; E is not read).
- * K % 8 == 0, E < 65536 else MOE355_EUNSUPPORTED; x, q, qt 16-byte aligned, ld_x and ld_q multiples of 8.
+ * K % 8 == 0 and up to 2^30, E < 65536 and (R/128 + E) * ceil(K/128) < 2^24 (without offsets ceil(R/128) in the sum's place), else
+ * MOE355_EUNSUPPORTED; x, q, qt 16-byte aligned, ld_x and ld_q multiples of 8.
  *
  * fp8_quant_128x128: weights w [E, N, K] -> q the same shape and scale [E, ceil(N/128), ceil(K/128)], one for each
  * 128 x 128: E8M0, or fp32 (e8m0 = 0; amax/448 and the quotients as in fp8_quant_1x128, NaN for a block that is not
  * finite).  qt and tscale (NULL for none) hold the same codes and scales transposed, [E, K, N] and
- * [E, ceil(K/128), ceil(N/128)].  K % 8 == 0 and with qt N % 16 == 0, else MOE355_EUNSUPPORTED.
+ * [E, ceil(K/128), ceil(N/128)].  K % 8 == 0, with qt N % 16 == 0, N and K up to 2^30 and fewer than 2^24 blocks,
+ * else MOE355_EUNSUPPORTED.
  */
 int fp8_ragged_blocks(int R, int E, int64_t* blocks);
 int fp8_quant_ragged(const uint16_t* x, int fp16, int64_t ld_x, const int32_t* offsets, int R, int E, int K,
@@ -521,7 +525,8 @@ int fp8_quant_128x128(const uint16_t* w, int fp16, int E, int N, int K, uint8_t*
  * multiplied first, so where their product is below 2^-126 a block is off by up to 2^-150 times its sum of |x8 * w8| (less than 2^-125),
  * and where it is 2^128 or more the block is infinite, or NaN if its sum is zero; with E8M0 scales what lies below 2^-126 may be lost.
  * grouped_gemm_fp8: N % 8 == 0, K % 16 == 0, ld_x and N up to 4194304, ld_y and sstride_m up to 2097152; wgrad: N % 8 == 0,
- * K % 8 == 0, both up to 4194304; E < 65536 and R up to 2^31 - 256; else MOE355_EUNSUPPORTED.  Pointers 16-byte aligned (fp32 scales and offsets 4,
+ * K % 8 == 0, both up to 4194304; E < 65536, R up to 2^31 - 256 and fewer than 2^31 tiles of the output (at least
+ * 32 x 64); else MOE355_EUNSUPPORTED.  Pointers 16-byte aligned (fp32 scales and offsets 4,
  * E8M0 scales any: they are read with the rest of the aligned 4 bytes that hold them), ld_x a multiple of 16 and ld_y of 8, else
  * MOE355_EMISALIGNED.
  */
